@@ -213,7 +213,8 @@ def work(case):
 
 def _to_half(v):
     """v >= 0 (64 bits) rounded once to the nearest fp16 value, ties to even."""
-    step = torch.ldexp(torch.ones_like(v), torch.frexp(v).exponent.clamp(min=-13) - 11)
+    e = torch.frexp(v).exponent.clamp(min=-13) - 11
+    step = (e.long() + 1023 << 52).view(torch.float64)      # 2^e from its bits: a device's pow(2, e) may be off
     return torch.round(v / step) * step
 
 
