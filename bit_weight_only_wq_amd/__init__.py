@@ -17,7 +17,10 @@ from ._lib import (WQ_PATH_AUTO, WQ_PATH_GEMV, WQ_PATH_MFMA, WQError,  # noqa: F
 
 __all__ = ["quantize_pack", "gemm", "gemm_grouped", "gemm_workspace_bytes", "codes_bytes", "num_groups",
            "gemv_max_batch",
-           "gemm_nf4", "gemm_offset", "KVCache", "kv_quantize_block", "kv_attention", "WQError", "LIB_PATH", "load"]
+           "gemm_nf4", "gemm_offset", "KVCache", "kv_quantize_block", "kv_attention",
+           "rope", "rope_frequencies", "PagedKV", "kv_paged_append", "kv_paged_attention", "kv_paged_workspace",
+           "kv_paged_copy", "kv_paged_fork", "kv_paged_compact", "kv_paged_compact_workspace",
+           "WQError", "LIB_PATH", "load"]
 
 _PATHS = {"auto": WQ_PATH_AUTO, "gemv": WQ_PATH_GEMV, "mfma": WQ_PATH_MFMA}
 
@@ -325,3 +328,333 @@ def dequantize(codes, scales, zeros, N: int, K: int, group: int = 128, bits: int
                                   bits, SCHEMES[scheme], out.data_ptr(), _stream_handle(codes.device))
     check(st, "wq_dequantize")
     return out
+
+
+# ---- rotary positions -----------------------------------------------------------
+
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+
+
+def _launch(where, device, fn, *args):
+    """fn(*args, stream) on `device` and its current stream."""
+    import torch
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, torch.cuda.current_stream().cuda_stream)
+    if st:
+        check(st, where)
+
+
+def _gpu(t, dtype, name, device=None):
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _line(t, dtype, n, name, device):
+    """A contiguous 1-D tensor of n values (n None: any number)."""
+    _gpu(t, dtype, name, device)
+    if t.dim() != 1 or (n is not None and t.shape[0] != n) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 1-D tensor" + (f" of {n}" if n is not None else "")
+                         + f", got shape {tuple(t.shape)}")
+
+
+def _rows_meet(a, b):
+    """Whether [T, H, D] tensors a and b (last stride 1) share memory, told from
+    their extents: rows of one token stride that lie side by side are apart."""
+    size = a.element_size()
+    extent = lambda t: sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1  # noqa: E731
+    ea, eb = extent(a), extent(b)
+    d = (b.data_ptr() - a.data_ptr()) / size
+    if d >= ea or -d >= eb:
+        return False
+    step = a.stride(0)
+    if step == b.stride(0) and step > 0:
+        ra, rb = (1 + (t.shape[1] - 1) * t.stride(1) + t.shape[2] - 1 for t in (a, b))
+        return not (ra <= d % step <= step - rb)
+    return True
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, kind: str = "none", factor: float = 1.0, context: int = 4096,
+                     low: float = 1.0, high: float = 32.0, device="cuda"):
+    """float64 [rot / 2]: radians per token of each pair, base^(-2j / rot), for a
+    context stretched by `factor`:
+      "none"    as they are
+      "linear"  all divided by factor
+      "base"    base multiplied by factor^(rot / (rot - 2)), which divides the
+                slowest pair by factor and leaves the fastest
+      "parts"   pairs that turn less than `low` times within `context` tokens
+                divided by factor, those of more than `high` turns left, those
+                between going over linearly in their turns."""
+    import math
+    import torch
+    if rot < 0 or rot % 2 or base <= 0 or factor <= 0 or kind not in ("none", "linear", "base", "parts"):
+        raise ValueError(f"rope_frequencies: need even rot >= 0, base > 0, factor > 0 and a known kind (rot={rot} "
+                         f"kind={kind!r})")
+    if kind == "base" and rot > 2:
+        base = base * factor ** (rot / (rot - 2))
+    f = torch.pow(torch.tensor(base, dtype=torch.float64), -torch.arange(0, rot, 2, dtype=torch.float64) / max(rot, 1))
+    if kind == "linear":
+        f = f / factor
+    elif kind == "parts":
+        keep = ((context * f / (2 * math.pi) - low) / (high - low)).clamp(0, 1)
+        f = f * keep + f / factor * (1 - keep)
+    return f.to(device)
+
+
+def rope(x, positions, freqs, layout: str = "half", scale: float = 1.0, out=None):
+    """Rotary positions: fp16 [tokens, heads, dim] x with every pair of the first
+    2 * len(freqs) channels turned by positions[token] * freqs[pair] radians
+    (int32 positions, float64 freqs) and multiplied by scale; further channels
+    are copied.  layout "half" pairs channels j and j + rot / 2, "interleaved"
+    2j and 2j + 1.  x may be a strided part of a packed row (last stride 1).
+    out: a tensor of x's shape, x itself for in place, or None for a new one."""
+    import torch
+    f16 = torch.float16
+    _gpu(x, f16, "x")
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"unknown layout {layout!r}")
+    if x.dim() != 3 or (x.shape[2] > 1 and x.stride(2) != 1):
+        raise ValueError("x must be [tokens, heads, dim] with contiguous channels")
+    T, H, dim = x.shape
+    dev = x.device
+    _line(positions, torch.int32, T, "positions", dev)
+    _line(freqs, torch.float64, None, "freqs", dev)
+    if out is None:
+        out = torch.empty((T, H, dim), dtype=f16, device=dev)
+    elif out is not x:
+        _gpu(out, f16, "out", dev)
+        if out.shape != x.shape or (dim > 1 and out.stride(2) != 1):
+            raise ValueError("out must have x's shape and contiguous channels")
+        if x.numel() and not (out.data_ptr() == x.data_ptr() and out.stride() == x.stride()) and _rows_meet(x, out):
+            raise ValueError("out overlaps x: only in place, with x's strides")
+    xs, os_ = x.stride(), out.stride()
+    _launch("wq_rope", dev, load().wq_rope, x.data_ptr(), T, H, dim, xs[0], xs[1], positions.data_ptr(),
+            freqs.data_ptr(), 2 * freqs.shape[0], ROPE_LAYOUTS[layout], scale, out.data_ptr(), os_[0], os_[1])
+    return out
+
+
+# ---- paged KV cache ---------------------------------------------------------------
+
+class PagedKV:
+    """Caller-owned buffers of one layer's paged int4 KV cache, as torch tensors
+    on one GPU; layout as wq_kv_paged in wq.h.  Either new, zeroed buffers of the
+    given sizes, or existing ones: pages u8 [num_pages, heads, 17408], windows
+    fp16 [slots, heads, 2, 128, 128], table int32 [slots, max_pages].
+
+        cache = PagedKV(heads=8, num_pages=4096, slots=64, max_pages=256)
+        cache.table[slot, block] = page        # which page a block will get
+        lens += 1                              # int32 [slots], after the append
+        kv_paged_append(k, v, cache, lens)     # the step's k (rotated) and v
+        out = kv_paged_attention(q, cache, lens)"""
+
+    D = 128
+    G = 128
+    RECORD = 17408
+
+    def __init__(self, heads=None, num_pages=None, slots=None, max_pages=None, device="cuda", *, pages=None,
+                 windows=None, table=None):
+        import torch
+        if pages is None:
+            pages = torch.zeros((num_pages, heads, self.RECORD), dtype=torch.uint8, device=device)
+        if windows is None:
+            windows = torch.zeros((slots, pages.shape[1], 2, self.G, self.D), dtype=torch.float16, device=pages.device)
+        if table is None:
+            table = torch.full((windows.shape[0], max_pages), -1, dtype=torch.int32, device=pages.device)
+        _gpu(pages, torch.uint8, "pages")
+        if pages.dim() != 3 or pages.shape[2] != self.RECORD or not pages.is_contiguous():
+            raise ValueError(f"pages must be contiguous [num_pages, heads, {self.RECORD}], got {tuple(pages.shape)}")
+        self.pages, self.device = pages, pages.device
+        self.num_pages, self.heads = pages.shape[0], pages.shape[1]
+        _gpu(windows, torch.float16, "windows", self.device)
+        if tuple(windows.shape[1:]) != (self.heads, 2, self.G, self.D) or not windows.is_contiguous():
+            raise ValueError(f"windows must be contiguous [slots, {self.heads}, 2, {self.G}, {self.D}], "
+                             f"got {tuple(windows.shape)}")
+        self.windows, self.slots = windows, windows.shape[0]
+        self.table = table
+
+    @property
+    def table(self):
+        return self._table
+
+    @table.setter
+    def table(self, table):
+        import ctypes
+        import torch
+        from ._lib import KvPaged
+        _gpu(table, torch.int32, "table", self.device)
+        if table.dim() != 2 or table.shape[0] != self.slots or not table.is_contiguous():
+            raise ValueError(f"table must be contiguous [{self.slots}, max_pages], got {tuple(table.shape)}")
+        self._table, self.max_pages = table, table.shape[1]
+        self._desc = KvPaged(self.pages.data_ptr(), self.windows.data_ptr(), table.data_ptr(), self.heads,
+                             self.num_pages, self.slots, self.max_pages)
+        self._ref = ctypes.byref(self._desc)
+
+    def descriptor(self):
+        return self._desc
+
+
+def _batch(cache, lens, seqs, count):
+    """Checks a call's lens and seqs; returns (seqs pointer, entries)."""
+    import torch
+    _line(lens, torch.int32, cache.slots, "lens", cache.device)
+    if seqs is None:
+        return None, count
+    _line(seqs, torch.int32, count, "seqs", cache.device)
+    return seqs.data_ptr(), seqs.shape[0]
+
+
+def _heads_rows(t, heads, name, device):
+    """Checks fp16 [rows, heads, 128] with a row's heads contiguous; returns its
+    row stride (heads None: any number)."""
+    import torch
+    _gpu(t, torch.float16, name, device)
+    if t.dim() != 3 or t.shape[2] != 128 or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [rows, {heads if heads is not None else 'heads'}, 128], got {tuple(t.shape)}")
+    n, h, _ = t.shape
+    st = t.stride()
+    if t.numel() and (st[2] != 1 or (h > 1 and st[1] != 128)):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return st[0] if n > 1 else h * 128
+
+
+def kv_paged_append(k, v, cache: PagedKV, lens, seqs=None, cu=None):
+    """Append new tokens: k, v fp16 [tokens, heads, 128] (rows may be strided
+    parts of a packed row).  lens int32 [slots]: tokens held AFTER the append.
+    seqs int32 [entries]: the slots of the entries (None: 0, 1, ..); cu int32
+    [entries + 1]: entry i brings tokens cu[i] .. cu[i + 1] - 1 (None: one
+    token each).  Blocks that become whole are quantized into the pages that
+    cache.table names; see wq_kv_paged_append in wq.h for what is left out."""
+    import torch
+    ks = _heads_rows(k, cache.heads, "k", cache.device)
+    vs = _heads_rows(v, cache.heads, "v", cache.device)
+    T = k.shape[0]
+    if v.shape[0] != T:
+        raise ValueError(f"k and v must have equally many tokens, got {T} and {v.shape[0]}")
+    if cu is None:
+        sp, n = _batch(cache, lens, seqs, T)
+        cp = None
+    else:
+        _line(cu, torch.int32, None, "cu", cache.device)
+        if cu.shape[0] < 1:
+            raise ValueError("cu must hold one value more than there are entries")
+        sp, n = _batch(cache, lens, seqs, cu.shape[0] - 1)
+        cp = cu.data_ptr()
+    _launch("wq_kv_paged_append", cache.device, load().wq_kv_paged_append, k.data_ptr(), v.data_ptr(), T, ks, vs,
+            cache._ref, lens.data_ptr(), sp, cp, n)
+
+
+def kv_paged_workspace(cache: PagedKV, count: int, q_heads: int):
+    """A workspace tensor for kv_paged_attention calls of this shape that do not
+    overlap (uint8, possibly empty)."""
+    import torch
+    with torch.cuda.device(cache.device):
+        need = _size_t(load().wq_kv_paged_workspace_size, cache._ref, count, q_heads, where="wq_kv_paged_attention")
+    return torch.empty(need, dtype=torch.uint8, device=cache.device)
+
+
+def _given(workspace, device):
+    """(pointer, bytes) of a caller's workspace tensor (its size is checked by the call)."""
+    import torch
+    if (not isinstance(workspace, torch.Tensor) or workspace.device != device or workspace.dtype != torch.uint8
+            or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
+    n = workspace.numel()
+    return (workspace.data_ptr(), n) if n else (None, 0)
+
+
+def kv_paged_attention(q, cache: PagedKV, lens, seqs=None, window: int = 0, scale=None, out=None, workspace=None,
+                       use_workspace=True):
+    """Decode attention of one new token per entry: q fp16 [entries, q_heads, 128]
+    (rows may be strided parts of a packed row), q_heads a multiple of
+    cache.heads -> out fp16 of the same shape, softmax(scale K q) V over the
+    tokens lens says each slot holds.  seqs as in kv_paged_append; window > 0
+    keeps the last `window` tokens; scale defaults to 1 / sqrt(128).  The
+    workspace comes from torch or from `workspace` (kv_paged_workspace);
+    use_workspace=False walks each sequence and KV head with one wavefront."""
+    import torch
+    dev = cache.device
+    qs = _heads_rows(q, None, "q", dev)
+    S, Hq, _ = q.shape
+    sp, n = _batch(cache, lens, seqs, S)
+    if out is None:
+        out = torch.empty((S, Hq, 128), dtype=torch.float16, device=dev)
+        os_ = Hq * 128
+    else:
+        os_ = _heads_rows(out, Hq, "out", dev)
+        if out.shape[0] != S:
+            raise ValueError(f"out must have q's shape {tuple(q.shape)}, got {tuple(out.shape)}")
+    if workspace is None and use_workspace:
+        workspace = kv_paged_workspace(cache, S, Hq)
+    wp, wn = _given(workspace, dev) if workspace is not None and use_workspace else (None, 0)
+    _launch("wq_kv_paged_attention", dev, load().wq_kv_paged_attention, q.data_ptr(), qs, Hq, cache._ref,
+            lens.data_ptr(), sp, n, window, 0.08838834764831845 if scale is None else scale, out.data_ptr(), os_, wp,
+            wn)
+    return out
+
+
+def _pairs(pairs):
+    """Host int32 [n, 2] of (source, destination) ids."""
+    import numpy as np
+    a = np.asarray(pairs)
+    if a.size == 0:
+        return np.zeros((0, 2), np.int32)
+    if a.ndim != 2 or a.shape[1] != 2 or a.dtype.kind not in "iu":
+        raise ValueError(f"pairs must be whole numbers [n, 2], got {a.dtype} {a.shape}")
+    if a.dtype != np.int32 and (a.min() < -2 ** 31 or a.max() > 2 ** 31 - 1):
+        raise ValueError("pairs: an id out of range")
+    return np.ascontiguousarray(a, dtype=np.int32)
+
+
+def kv_paged_copy(cache: PagedKV, pairs):
+    """Copy whole pages: pairs, on the host, of (source, destination) page ids
+    (an int32 array [n, 2], or a list); no destination twice, none a source."""
+    a = _pairs(pairs)
+    _launch("wq_kv_paged_copy", cache.device, load().wq_kv_paged_copy, cache._ref, a.ctypes.data, a.shape[0])
+
+
+def kv_paged_fork(cache: PagedKV, lens, pairs):
+    """Fork sequences: for each (source, destination) slot of the host pairs the
+    destination becomes a second holder of the source's tokens (whole blocks
+    shared through the table, the window's tokens copied, lens set)."""
+    import torch
+    a = _pairs(pairs)
+    _line(lens, torch.int32, cache.slots, "lens", cache.device)
+    _launch("wq_kv_paged_fork", cache.device, load().wq_kv_paged_fork, cache._ref, lens.data_ptr(), a.ctypes.data,
+            a.shape[0])
+
+
+def kv_paged_compact_workspace(cache: PagedKV):
+    """A workspace tensor for kv_paged_compact of this cache."""
+    import torch
+    need = _size_t(load().wq_kv_paged_compact_workspace_size, cache._ref, where="wq_kv_paged_compact")
+    return torch.empty(need, dtype=torch.uint8, device=cache.device)
+
+
+def kv_paged_compact(cache: PagedKV, lens, out=None, workspace=None):
+    """Move the pages in use (those the table names for the whole blocks of lens)
+    to ids 0 .. used - 1.  Returns (table, used): the new int32 table, and int32
+    [1] on the GPU.  cache.table is not changed: set cache.table = table to go
+    on with the packed pool.  out: such a pair to write into."""
+    import torch
+    dev = cache.device
+    _line(lens, torch.int32, cache.slots, "lens", dev)
+    if out is None:
+        table = torch.empty((cache.slots, cache.max_pages), dtype=torch.int32, device=dev)
+        used = torch.empty(1, dtype=torch.int32, device=dev)
+    else:
+        table, used = out
+        _need(table, torch.int32, (cache.slots, cache.max_pages), "table")
+        _line(used, torch.int32, 1, "used", dev)
+        if table.device != dev:
+            raise ValueError(f"table must be on {dev}")
+    wp, wn = _given(kv_paged_compact_workspace(cache) if workspace is None else workspace, dev)
+    _launch("wq_kv_paged_compact", dev, load().wq_kv_paged_compact, cache._ref, lens.data_ptr(), table.data_ptr(),
+            used.data_ptr(), wp, wn)
+    return table, used

@@ -24,6 +24,11 @@ WQ_SCHEME_SYM_TENSOR = 2
 WQ_SCHEME_NF4 = 3
 WQ_SCHEME_OFFSET = 4
 
+WQ_ROPE_HALF = 0
+WQ_ROPE_INTERLEAVED = 1
+
+WQ_KV_RECORD_BYTES = 17408
+
 # Every symbol include/wq.h declares, with (restype, argtypes).
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -44,6 +49,14 @@ class KvCache(ctypes.Structure):
                 ("heads", _I64), ("max_blocks", _I64)]
 
 
+class KvPaged(ctypes.Structure):
+    """wq_kv_paged: the buffers of a paged int4 KV cache (device pointers)."""
+    _fields_ = [("pages", _P), ("windows", _P), ("table", _P), ("heads", _I64), ("num_pages", _I64),
+                ("slots", _I64), ("max_pages", _I64)]
+
+
+_PAGED = ctypes.POINTER(KvPaged)
+
 SIGNATURES = {
     "wq_quantize_pack": (ctypes.c_int, [_P, _I64, _I64, _I32, _I32, _P, _P, _P, _P]),
     "wq_quantize_pack_ex": (ctypes.c_int, [_P, _I64, _I64, _I32, _I32, _I32, _P, _P, _P, _P, _SZ, _P]),
@@ -57,6 +70,16 @@ SIGNATURES = {
     "wq_kv_quantize_block": (ctypes.c_int, [_P, _P, ctypes.POINTER(KvCache), _I64, _P]),
     "wq_kv_attention": (ctypes.c_int, [_P, ctypes.POINTER(KvCache), _P, _P, _P, _SZ, _P]),
     "wq_kv_workspace_size": (ctypes.c_int, [ctypes.POINTER(KvCache), ctypes.POINTER(_SZ)]),
+    "wq_rope": (ctypes.c_int, [_P, _I64, _I64, _I64, _I64, _I64, _P, _P, _I64, _I32, ctypes.c_float, _P,
+                               _I64, _I64, _P]),
+    "wq_kv_paged_append": (ctypes.c_int, [_P, _P, _I64, _I64, _I64, _PAGED, _P, _P, _P, _I64, _P]),
+    "wq_kv_paged_attention": (ctypes.c_int, [_P, _I64, _I64, _PAGED, _P, _P, _I64, _I64, ctypes.c_float, _P,
+                                             _I64, _P, _SZ, _P]),
+    "wq_kv_paged_workspace_size": (ctypes.c_int, [_PAGED, _I64, _I64, ctypes.POINTER(_SZ)]),
+    "wq_kv_paged_copy": (ctypes.c_int, [_PAGED, _P, _I64, _P]),
+    "wq_kv_paged_fork": (ctypes.c_int, [_PAGED, _P, _P, _I64, _P]),
+    "wq_kv_paged_compact": (ctypes.c_int, [_PAGED, _P, _P, _P, _P, _SZ, _P]),
+    "wq_kv_paged_compact_workspace_size": (ctypes.c_int, [_PAGED, ctypes.POINTER(_SZ)]),
     "wq_gemm_nf4": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I64, _I64, _I32, _P]),
     "wq_gemm_offset": (ctypes.c_int, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _I32, _P]),
     "wq_dequantize": (ctypes.c_int, [_P, _P, _P, _I64, _I64, _I32, _I32, _I32, _P, _P]),

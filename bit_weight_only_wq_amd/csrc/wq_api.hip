@@ -8,6 +8,7 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <algorithm>
 #include <mutex>
 #include <new>
 
@@ -585,6 +586,264 @@ wq_status wq_kv_attention(const void* q, const wq_kv_cache* cache, const int32_t
     ws.ptr = need > 0 ? workspace : nullptr;
     return check_hip(wq::launch_kv_attention(q, a, lens, out, num_cus(), ws, static_cast<hipStream_t>(stream)),
                      "wq_kv_attention launch");
+}
+
+// ---- rotary positions ------------------------------------------------------------
+
+// Whether rows of `dim` elements at t * ts + h * hs never overlap.
+static bool rows_apart(int64_t tokens, int64_t heads, int64_t dim, int64_t ts, int64_t hs) {
+    if (heads > 1 && hs < dim) return false;
+    if (tokens <= 1) return true;
+    return ts >= (heads - 1) * hs + dim || (ts >= dim && (heads <= 1 || hs >= (tokens - 1) * ts + dim));
+}
+
+wq_status wq_rope(const void* x, int64_t tokens, int64_t heads, int64_t dim, int64_t x_token_stride,
+                  int64_t x_head_stride, const int32_t* positions, const double* freqs, int64_t rot,
+                  int32_t layout, float scale, void* out, int64_t out_token_stride, int64_t out_head_stride,
+                  void* stream) {
+    g_last_error[0] = '\0';
+    if (tokens < 0 || heads < 0 || dim < 1 || rot < 0 || rot > dim || rot % 2 != 0)
+        return fail(WQ_ERR_INVALID_ARG, "wq_rope: need tokens, heads >= 0, dim >= 1, even rot in [0, dim] (dim=%lld "
+                    "rot=%lld)", dim, rot);
+    if (layout != WQ_ROPE_HALF && layout != WQ_ROPE_INTERLEAVED)
+        return fail(WQ_ERR_INVALID_ARG, "wq_rope: unknown layout %lld", layout);
+    if (dim > 1024 || tokens >= ((int64_t)1 << 24) || heads > 65535)
+        return fail(WQ_ERR_UNSUPPORTED, "wq_rope: dim <= 1024, tokens < 2^24, heads <= 65535 (tokens=%lld heads=%lld)",
+                    tokens, heads);
+    const int64_t far = (int64_t)1 << 37;    // offsets stay far inside 64 bits
+    if (x_token_stride < 0 || x_head_stride < 0 || x_token_stride > far || x_head_stride > far ||
+        out_token_stride < 0 || out_head_stride < 0 || out_token_stride > far || out_head_stride > far)
+        return fail(WQ_ERR_INVALID_ARG, "wq_rope: strides must be in [0, 2^37]");
+    if (tokens == 0 || heads == 0) return WQ_OK;
+    if (!rows_apart(tokens, heads, dim, out_token_stride, out_head_stride))
+        return fail(WQ_ERR_INVALID_ARG, "wq_rope: output strides (%lld, %lld) make heads overlap", out_token_stride,
+                    out_head_stride);
+    if (x == out && ((tokens > 1 && x_token_stride != out_token_stride) || (heads > 1 && x_head_stride != out_head_stride)))
+        return fail(WQ_ERR_INVALID_ARG, "wq_rope: in place needs equal strides");
+    if (!x || !out || (rot > 0 && (!positions || !freqs))) return fail(WQ_ERR_INVALID_ARG, "wq_rope: null pointer");
+    if (!aligned(x, 2) || !aligned(out, 2) || !aligned(positions, 4) || !aligned(freqs, 8))
+        return fail(WQ_ERR_MISALIGNED, "wq_rope: x and out need 2-byte, positions 4-byte, freqs 8-byte alignment");
+    const wq::RopeCall c{x, out, positions, freqs, tokens, heads, dim, rot, x_token_stride, x_head_stride,
+                         out_token_stride, out_head_stride, layout == WQ_ROPE_HALF, scale};
+    return check_hip(wq::launch_rope(c, num_cus(), static_cast<hipStream_t>(stream)), "wq_rope launch");
+}
+
+// ---- paged KV cache --------------------------------------------------------------
+
+// Validates a descriptor's sizes, and the buffers named in `need` (1 pages,
+// 2 windows, 4 table), and copies it into `a`.
+static wq_status check_paged(const wq_kv_paged* c, wq::PagedArgs& a, int need) {
+    if (!c) return fail(WQ_ERR_INVALID_ARG, "paged kv cache: null descriptor");
+    const int64_t top = ((int64_t)1 << 31) - 1;
+    if (c->heads < 1 || c->heads > 32767 || c->num_pages < 1 || c->num_pages > top || c->slots < 1 ||
+        c->slots > top)
+        return fail(WQ_ERR_INVALID_ARG, "paged kv cache: need 1 <= heads <= 32767 and 1 <= num_pages, slots < 2^31 "
+                    "(heads=%lld num_pages=%lld)", c->heads, c->num_pages);
+    if (c->max_pages < 1 || c->max_pages > ((int64_t)1 << 24) - 1)
+        return fail(WQ_ERR_INVALID_ARG, "paged kv cache: need 1 <= max_pages < 2^24 (max_pages=%lld)", c->max_pages);
+    if (((need & 1) && !c->pages) || ((need & 2) && !c->windows) || ((need & 4) && !c->table))
+        return fail(WQ_ERR_INVALID_ARG, "paged kv cache: null buffer");
+    if (((need & 1) && !aligned(c->pages, 16)) || ((need & 2) && !aligned(c->windows, 16)) ||
+        ((need & 4) && !aligned(c->table, 4)))
+        return fail(WQ_ERR_MISALIGNED, "paged kv cache: pages and windows need 16-byte, table 4-byte alignment");
+    a = wq::PagedArgs{c->pages, c->windows, static_cast<const int32_t*>(c->table), c->heads, c->num_pages, c->slots,
+                      c->max_pages};
+    return WQ_OK;
+}
+
+// Entries of a call's batch.
+static wq_status check_batch(const char* who, const wq::PagedArgs& a, const int32_t* lens, const int32_t* seqs,
+                             int64_t count) {
+    if (count < 0 || count > 65535 || (!seqs && count > a.slots)) {
+        snprintf(g_last_error, sizeof(g_last_error), "%s: count=%lld outside [0, 65535], or past the %lld slots", who,
+                 (long long)count, (long long)a.slots);
+        return WQ_ERR_INVALID_ARG;
+    }
+    if (count > 0 && (!lens || !aligned(lens, 4) || !aligned(seqs, 4))) {
+        snprintf(g_last_error, sizeof(g_last_error), "%s: null or misaligned lens or seqs", who);
+        return lens ? WQ_ERR_MISALIGNED : WQ_ERR_INVALID_ARG;
+    }
+    return WQ_OK;
+}
+
+wq_status wq_kv_paged_append(const void* k, const void* v, int64_t tokens, int64_t k_stride, int64_t v_stride,
+                             const wq_kv_paged* cache, const int32_t* lens, const int32_t* seqs, const int32_t* cu,
+                             int64_t count, void* stream) {
+    g_last_error[0] = '\0';
+    wq::PagedArgs a;
+    wq_status st = check_paged(cache, a, 7);
+    if (st != WQ_OK) return st;
+    st = check_batch("wq_kv_paged_append", a, lens, seqs, count);
+    if (st != WQ_OK) return st;
+    if (tokens < 0 || tokens > ((int64_t)1 << 30) || (!cu && tokens != count))
+        return fail(WQ_ERR_INVALID_ARG, "wq_kv_paged_append: tokens=%lld for %lld entries (without cu: one each)", tokens,
+                    count);
+    if (count == 0 || tokens == 0) return WQ_OK;
+    const int64_t row = a.heads * 128;
+    if (k_stride < row || v_stride < row || k_stride > ((int64_t)1 << 31) || v_stride > ((int64_t)1 << 31))
+        return fail(WQ_ERR_INVALID_ARG, "wq_kv_paged_append: k_stride=%lld and v_stride=%lld must hold a token's heads",
+                    k_stride, v_stride);
+    if (!k || !v) return fail(WQ_ERR_INVALID_ARG, "wq_kv_paged_append: null k or v");
+    if (!aligned(k, 16) || !aligned(v, 16) || k_stride % 8 != 0 || v_stride % 8 != 0 || !aligned(cu, 4))
+        return fail(WQ_ERR_MISALIGNED, "wq_kv_paged_append: k, v and their strides need 16-byte, cu 4-byte alignment");
+    return check_hip(wq::launch_paged_append(k, v, tokens, k_stride, v_stride, a, lens, seqs, cu, count,
+                                             static_cast<hipStream_t>(stream)),
+                     "wq_kv_paged_append launch");
+}
+
+// Shape checks of an attention call (no pointers but the descriptor).
+static wq_status check_paged_attention(const wq::PagedArgs& a, int64_t count, int64_t q_heads) {
+    if (count < 0 || count > 65535 || q_heads < a.heads || q_heads % a.heads != 0)
+        return fail(WQ_ERR_INVALID_ARG, "wq_kv_paged_attention: need 0 <= count <= 65535 and q_heads a multiple of the "
+                    "cache's heads (count=%lld q_heads=%lld)", count, q_heads);
+    if (q_heads > 65535 || count * q_heads > (((int64_t)1 << 31) - 1) / (a.max_pages + 4))
+        return fail(WQ_ERR_UNSUPPORTED, "wq_kv_paged_attention: count * q_heads * (max_pages + 4) must be below 2^31 and "
+                    "q_heads below 2^16 (count=%lld q_heads=%lld)", count, q_heads);
+    return WQ_OK;
+}
+
+wq_status wq_kv_paged_workspace_size(const wq_kv_paged* cache, int64_t count, int64_t q_heads, size_t* bytes) {
+    g_last_error[0] = '\0';
+    if (!bytes) return fail(WQ_ERR_INVALID_ARG, "wq_kv_paged_workspace_size: null bytes");
+    *bytes = 0;
+    wq::PagedArgs a;
+    wq_status st = check_paged(cache, a, 0);
+    if (st == WQ_OK) st = check_paged_attention(a, count, q_heads);
+    if (st != WQ_OK || count == 0) return st;
+    size_t need = 0;
+    wq::Scratch ws;
+    ws.need = &need;
+    st = check_hip(wq::launch_paged_attention(nullptr, 0, q_heads, a, nullptr, nullptr, count, 0, 1.0f, nullptr, 0,
+                                              num_cus(), ws, nullptr),
+                   "wq_kv_paged_workspace_size");
+    if (st == WQ_OK) *bytes = need;
+    return st;
+}
+
+wq_status wq_kv_paged_attention(const void* q, int64_t q_stride, int64_t q_heads, const wq_kv_paged* cache,
+                                const int32_t* lens, const int32_t* seqs, int64_t count, int64_t window, float scale,
+                                void* out, int64_t out_stride, void* workspace, size_t workspace_bytes, void* stream) {
+    g_last_error[0] = '\0';
+    wq::PagedArgs a;
+    wq_status st = check_paged(cache, a, 7);
+    if (st == WQ_OK) st = check_paged_attention(a, count, q_heads);
+    if (st == WQ_OK) st = check_batch("wq_kv_paged_attention", a, lens, seqs, count);
+    if (st != WQ_OK) return st;
+    const int64_t far = (int64_t)1 << 31, row = q_heads * 128;
+    if (window < 0 || !(scale - scale == 0.0f))
+        return fail(WQ_ERR_INVALID_ARG, "wq_kv_paged_attention: window=%lld must be >= 0, and scale finite", window);
+    if (count > 0 && (q_stride < row || out_stride < row || q_stride > far || out_stride > far))
+        return fail(WQ_ERR_INVALID_ARG, "wq_kv_paged_attention: q_stride=%lld and out_stride=%lld must hold an entry's "
+                    "heads", q_stride, out_stride);
+    size_t need = 0;
+    if (workspace && count > 0) {
+        wq::Scratch sz;
+        sz.need = &need;
+        st = check_hip(wq::launch_paged_attention(nullptr, 0, q_heads, a, nullptr, nullptr, count, 0, scale, nullptr, 0,
+                                                  num_cus(), sz, nullptr),
+                       "wq_kv_paged_attention sizing");
+        if (st != WQ_OK) return st;
+    }
+    st = check_workspace("wq_kv_paged_attention", workspace, workspace_bytes, need);
+    if (st != WQ_OK) return st;
+    if (count == 0) return WQ_OK;
+    if (!q || !out) return fail(WQ_ERR_INVALID_ARG, "wq_kv_paged_attention: null q or out");
+    if (!aligned(q, 16) || q_stride % 8 != 0 || !aligned(out, 8) || out_stride % 4 != 0)
+        return fail(WQ_ERR_MISALIGNED, "wq_kv_paged_attention: q and its stride need 16-byte, out and its stride 8-byte "
+                    "alignment");
+    wq::Scratch ws;
+    ws.ptr = need > 0 ? workspace : nullptr;
+    return check_hip(wq::launch_paged_attention(q, q_stride, q_heads, a, lens, seqs, count, window, scale, out, out_stride,
+                                                num_cus(), ws, static_cast<hipStream_t>(stream)),
+                     "wq_kv_paged_attention launch");
+}
+
+// Pairs of ids below `limit`: in range, no destination twice, none a source.
+static wq_status check_pairs(const char* who, const int32_t* pairs, int64_t count, int64_t limit) {
+    if (count < 0 || (count > 0 && !pairs)) {
+        snprintf(g_last_error, sizeof(g_last_error), "%s: null pairs or count=%lld", who, (long long)count);
+        return WQ_ERR_INVALID_ARG;
+    }
+    if (count == 0) return WQ_OK;
+    int32_t* ids = new (std::nothrow) int32_t[2 * (size_t)count];
+    if (!ids) return fail(WQ_ERR_INVALID_ARG, "paged kv cache: out of host memory (count=%lld)", count);
+    int32_t* dst = ids + count;
+    int64_t bad = -1;
+    for (int64_t i = 0; i < count && bad < 0; ++i) {
+        ids[i] = pairs[2 * i];
+        dst[i] = pairs[2 * i + 1];
+        if (ids[i] < 0 || dst[i] < 0 || ids[i] >= limit || dst[i] >= limit) bad = i;
+    }
+    const char* what = "an id out of range";
+    if (bad < 0) {
+        std::sort(ids, ids + count);
+        std::sort(dst, dst + count);
+        for (int64_t i = 0; i < count && bad < 0; ++i) {
+            if (i > 0 && dst[i] == dst[i - 1]) {
+                bad = dst[i];
+                what = "a destination twice:";
+            } else if (std::binary_search(ids, ids + count, dst[i])) {
+                bad = dst[i];
+                what = "a destination that is a source:";
+            }
+        }
+    }
+    delete[] ids;
+    if (bad < 0) return WQ_OK;
+    snprintf(g_last_error, sizeof(g_last_error), "%s: %s %lld", who, what, (long long)bad);
+    return WQ_ERR_INVALID_ARG;
+}
+
+wq_status wq_kv_paged_copy(const wq_kv_paged* cache, const int32_t* pairs, int64_t count, void* stream) {
+    g_last_error[0] = '\0';
+    wq::PagedArgs a;
+    wq_status st = check_paged(cache, a, 1);
+    if (st == WQ_OK) st = check_pairs("wq_kv_paged_copy", pairs, count, a.num_pages);
+    if (st != WQ_OK || count == 0) return st;
+    return check_hip(wq::launch_paged_copy(a, pairs, count, static_cast<hipStream_t>(stream)), "wq_kv_paged_copy launch");
+}
+
+wq_status wq_kv_paged_fork(const wq_kv_paged* cache, int32_t* lens, const int32_t* pairs, int64_t count, void* stream) {
+    g_last_error[0] = '\0';
+    wq::PagedArgs a;
+    wq_status st = check_paged(cache, a, 6);
+    if (st == WQ_OK) st = check_pairs("wq_kv_paged_fork", pairs, count, a.slots);
+    if (st != WQ_OK || count == 0) return st;
+    if (!lens) return fail(WQ_ERR_INVALID_ARG, "wq_kv_paged_fork: null lens");
+    if (!aligned(lens, 4)) return fail(WQ_ERR_MISALIGNED, "wq_kv_paged_fork: lens need 4-byte alignment");
+    return check_hip(wq::launch_paged_fork(a, lens, pairs, count, static_cast<hipStream_t>(stream)),
+                     "wq_kv_paged_fork launch");
+}
+
+wq_status wq_kv_paged_compact_workspace_size(const wq_kv_paged* cache, size_t* bytes) {
+    g_last_error[0] = '\0';
+    if (!bytes) return fail(WQ_ERR_INVALID_ARG, "wq_kv_paged_compact_workspace_size: null bytes");
+    *bytes = 0;
+    wq::PagedArgs a;
+    const wq_status st = check_paged(cache, a, 0);
+    if (st == WQ_OK) *bytes = wq::paged_compact_bytes(a);
+    return st;
+}
+
+wq_status wq_kv_paged_compact(const wq_kv_paged* cache, const int32_t* lens, void* table_out, int32_t* used,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+    g_last_error[0] = '\0';
+    wq::PagedArgs a;
+    wq_status st = check_paged(cache, a, 5);
+    if (st != WQ_OK) return st;
+    const size_t need = wq::paged_compact_bytes(a);
+    st = check_workspace("wq_kv_paged_compact", workspace, workspace_bytes, need);
+    if (st != WQ_OK) return st;
+    if (!workspace)
+        return fail(WQ_ERR_INVALID_ARG, "wq_kv_paged_compact: needs a workspace of %lld bytes", (long long)need);
+    if (!lens || !table_out || !used) return fail(WQ_ERR_INVALID_ARG, "wq_kv_paged_compact: null pointer");
+    if (!aligned(lens, 4) || !aligned(table_out, 4) || !aligned(used, 4))
+        return fail(WQ_ERR_MISALIGNED, "wq_kv_paged_compact: lens, table_out and used need 4-byte alignment");
+    if (table_out == cache->table)
+        return fail(WQ_ERR_INVALID_ARG, "wq_kv_paged_compact: table_out must not be the cache's table");
+    return check_hip(wq::launch_paged_compact(a, lens, static_cast<int32_t*>(table_out), used, workspace, num_cus(),
+                                              static_cast<hipStream_t>(stream)),
+                     "wq_kv_paged_compact launch");
 }
 
 // ---- other weight formats ------------------------------------------------------

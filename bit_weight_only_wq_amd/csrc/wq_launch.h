@@ -164,4 +164,39 @@ hipError_t launch_kv_attention(const void* q, const KvCacheArgs& c, const int32_
 hipError_t launch_kv_quantize(const void* K, const void* V, const KvCacheArgs& c, int64_t block,
                               hipStream_t stream);
 
+// Rotary positions (wq_rope.hip).  Strides in elements.
+struct RopeCall {
+    const void* x;
+    void* out;
+    const int32_t* positions;
+    const double* freqs;
+    int64_t tokens, heads, dim, rot, xt, xh, ot, oh;
+    bool half_layout;
+    float scale;
+};
+hipError_t launch_rope(const RopeCall& c, int num_cus, hipStream_t stream);
+
+// Paged int4 KV cache (layout in wq_paged.h; wq_kv_paged in wq.h).
+struct PagedArgs {
+    void* pages;
+    void* windows;
+    const int32_t* table;
+    int64_t heads, num_pages, slots, max_pages;
+};
+// (source, destination) ids of one launch, passed by value.
+constexpr int kPairsPerLaunch = 448;
+hipError_t launch_paged_append(const void* k, const void* v, int64_t tokens, int64_t k_stride, int64_t v_stride,
+                               const PagedArgs& c, const int32_t* lens, const int32_t* seqs, const int32_t* cu,
+                               int64_t count, hipStream_t stream);
+hipError_t launch_paged_attention(const void* q, int64_t q_stride, int64_t q_heads, const PagedArgs& c,
+                                  const int32_t* lens, const int32_t* seqs, int64_t count, int64_t window,
+                                  float scale, void* out, int64_t out_stride, int num_cus, const Scratch& ws,
+                                  hipStream_t stream);
+hipError_t launch_paged_copy(const PagedArgs& c, const int32_t* pairs, int64_t count, hipStream_t stream);
+hipError_t launch_paged_fork(const PagedArgs& c, int32_t* lens, const int32_t* pairs, int64_t count,
+                             hipStream_t stream);
+size_t paged_compact_bytes(const PagedArgs& c);
+hipError_t launch_paged_compact(const PagedArgs& c, const int32_t* lens, int32_t* table_out, int32_t* used,
+                                void* scratch, int num_cus, hipStream_t stream);
+
 }  // namespace wq

@@ -399,6 +399,174 @@ wq_status wq_kv_attention(const void* q, const wq_kv_cache* cache, const int32_t
  * (only heads and max_blocks are read; 0: none). */
 wq_status wq_kv_workspace_size(const wq_kv_cache* cache, size_t* bytes);
 
+/*
+ * Rotary positions: every pair of channels of every head of a token is turned
+ * by an angle that grows with the token's position, so that a score of two
+ * rotated vectors depends on how far apart they are.  With pair j < rot / 2 of
+ * a head's first `rot` channels, a = positions[t] * freqs[j] radians,
+ *     (u, w) -> (u cos a - w sin a, u sin a + w cos a) * scale,
+ * WQ_ROPE_HALF pairs channels j and j + rot / 2, WQ_ROPE_INTERLEAVED channels
+ * 2j and 2j + 1; channels rot .. dim - 1 are copied.  Frequencies and scale
+ * are the caller's, so any stretching of the context (linear, by parts, by
+ * base) is a table.  Angles are formed in 64 bits and reduced before the sine,
+ * so far positions keep their precision; the rotation is in fp32, rounded
+ * once to fp16.  Keys are rotated before they are cached.
+ *
+ * x          fp16; element (token, head, channel) at
+ *            token * x_token_stride + head * x_head_stride + channel
+ * positions  int32 [tokens], any value (a negative position turns back)
+ * freqs      float64 [rot / 2], radians per token
+ * out        fp16, its own strides (in elements); the same buffer with the
+ *            same strides as x rotates in place, any other overlap is not
+ *            allowed, and neither are output strides that make two heads
+ *            overlap (WQ_ERR_INVALID_ARG)
+ * tokens, heads >= 0 (0 is a no-op; tokens < 2^24, heads <= 65535), 1 <= dim
+ * <= 1024, 0 <= rot <= dim even; strides >= 0.  x and out 2-byte aligned; with 16-byte aligned buffers and
+ * strides, dim a multiple of 8 and rot of 16 (half) or 8 (interleaved), loads
+ * and stores are 16 bytes wide.
+ */
+typedef enum {
+    WQ_ROPE_HALF = 0,
+    WQ_ROPE_INTERLEAVED = 1
+} wq_rope_layout;
+
+wq_status wq_rope(const void* x, int64_t tokens, int64_t heads, int64_t dim, int64_t x_token_stride,
+                  int64_t x_head_stride, const int32_t* positions, const double* freqs, int64_t rot,
+                  int32_t layout, float scale, void* out, int64_t out_token_stride,
+                  int64_t out_head_stride, void* stream);
+
+/*
+ * Paged int4 KV cache: the codec and blocks of wq_kv_cache, for many sequences
+ * that grow one by one.  Head dimension 128, blocks of 128 tokens.
+ *   pages    u8 [num_pages][heads][17408], one record per page and KV head:
+ *            bytes     0  K codes u8 [128 tokens][64]   (layout of kcodes)
+ *                   8192  V codes u8 [128 channels][64] (layout of vcodes)
+ *                  16384  K scales fp16 [128 channels]
+ *                  16640  K zeros  fp16 [128 channels]
+ *                  16896  V scales fp16 [128 tokens]
+ *                  17152  V zeros  fp16 [128 tokens]
+ *   windows  fp16 [slots][heads][2][128][128] (0: K, 1: V), token-major: the
+ *            newest tokens of a slot's sequence, those past its whole blocks
+ *   table    int32 [slots][max_pages]: the page of each whole block of the
+ *            slot's sequence; entries past them are not read
+ * 1 <= heads <= 32767; num_pages, slots, max_pages >= 1.
+ * A slot holds one sequence; `lens` int32 [slots] says how many tokens (0:
+ * none), 0 <= lens <= max_pages * 128 + 127.  The first lens / 128 blocks are
+ * in pages, the other lens % 128 tokens in the slot's window.  Whole blocks
+ * never change, so sequences may share pages.  The caller owns every buffer
+ * and decides which page a block gets; pages, windows 16-byte aligned, table
+ * 4-byte aligned.  `seqs` int32 [count] names the slots of a call's batch in
+ * order (NULL: slots 0 .. count - 1); an entry outside [0, slots) is padding.
+ * lens, seqs, cu and table are DEVICE memory, so a captured graph follows
+ * their values.  All ids are checked on the device before they address memory.
+ */
+typedef struct wq_kv_paged {
+    void* pages;
+    void* windows;
+    void* table;
+    int64_t heads;
+    int64_t num_pages;
+    int64_t slots;
+    int64_t max_pages;
+} wq_kv_paged;
+
+#define WQ_KV_RECORD_BYTES 17408
+
+/*
+ * Append new tokens to `count` sequences.  `lens` holds the lengths AFTER the
+ * append (one array serves the appends and the attention of a step's layers):
+ * entry i brings n tokens, which become positions lens - n .. lens - 1 of its
+ * slot.  cu int32 [count + 1]: entry i brings tokens cu[i] .. cu[i + 1] - 1 of
+ * k and v; NULL: one token each (tokens == count).  Every block that becomes
+ * whole is quantized into page table[slot][block], codes and headers bit for
+ * bit those of wq_kv_quantize_block; the tokens after the last whole block go
+ * to the slot's window.  Nothing else is written.
+ *
+ * k, v     fp16 [tokens][heads][128], 16-byte aligned, k_stride and v_stride
+ *          elements from token to token (multiples of 8, >= heads * 128), so
+ *          they may be parts of one packed q/k/v row
+ * An entry is left out (nothing of it written) where it is padding, where its
+ * slot stands earlier in seqs (the first one counts), where its part of cu is
+ * not inside [0, tokens], or where lens < n or lens is past the slot's
+ * capacity; a block whose page is outside [0, num_pages) is not written.  Two
+ * blocks given the same page leave it undefined; a cu that does not ascend
+ * leaves out entries, whole or in part.  count or tokens == 0 is a no-op;
+ * count <= 65535, tokens <= 2^30.
+ */
+wq_status wq_kv_paged_append(const void* k, const void* v, int64_t tokens, int64_t k_stride,
+                             int64_t v_stride, const wq_kv_paged* cache, const int32_t* lens,
+                             const int32_t* seqs, const int32_t* cu, int64_t count, void* stream);
+
+/*
+ * Decode attention of one new token per sequence over the paged cache:
+ *     out[i, g] = softmax(scale * K_h q[i, g]) V_h,  h = g / (q_heads / heads)
+ * over the tokens that entry i's slot holds (the new one appended before),
+ * dequantized as (c - z) * s; window > 0 keeps the last `window` tokens only.
+ * q_heads is a multiple of heads.  No token to see (an empty or padded entry)
+ * gives zeros; lens are clamped to [0, max_pages * 128 + 127]; a table entry
+ * outside [0, num_pages) among the blocks that are read gives NaN in that
+ * entry's rows.
+ *
+ * q, out   fp16 [count][q_heads][128], q_stride and out_stride elements from
+ *          one entry to the next (>= q_heads * 128); q 16-byte aligned with
+ *          q_stride a multiple of 8, out 8-byte aligned with out_stride a
+ *          multiple of 4
+ * fp32 scores, softmax and sums.  Results do not depend on timing (no
+ * atomics), but on the batch: the work of all entries is cut into equal parts,
+ * and where a part ends inside a sequence, its sums are joined by a second
+ * kernel through the workspace (wq_kv_paged_workspace_size).  Without a
+ * workspace one wavefront walks each sequence and KV head.
+ * count <= 65535, count * q_heads * (max_pages + 4) < 2^31
+ * (WQ_ERR_UNSUPPORTED).
+ */
+wq_status wq_kv_paged_attention(const void* q, int64_t q_stride, int64_t q_heads,
+                                const wq_kv_paged* cache, const int32_t* lens, const int32_t* seqs,
+                                int64_t count, int64_t window, float scale, void* out,
+                                int64_t out_stride, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/* Workspace bytes of wq_kv_paged_attention for this cache, count and q_heads
+ * on the current device (no buffer is read; 0: none). */
+wq_status wq_kv_paged_workspace_size(const wq_kv_paged* cache, int64_t count, int64_t q_heads,
+                                     size_t* bytes);
+
+/*
+ * Copy whole pages: pairs is a HOST array of `count` (source, destination)
+ * page ids, read during the call.  Ids lie in [0, num_pages), no destination
+ * stands twice and none is a source (WQ_ERR_INVALID_ARG otherwise).  Only
+ * pages, heads and num_pages of the cache are used.
+ */
+wq_status wq_kv_paged_copy(const wq_kv_paged* cache, const int32_t* pairs, int64_t count, void* stream);
+
+/*
+ * Fork sequences: for each (source, destination) pair of slots (a HOST array,
+ * read during the call; no destination twice, none a source) the destination
+ * becomes a second holder of the source's tokens.  Whole blocks are shared:
+ * their table entries are copied.  The window's tokens are copied, and
+ * lens[destination] is set.  Table entries and window rows past the source's
+ * tokens stay as they were.
+ */
+wq_status wq_kv_paged_fork(const wq_kv_paged* cache, int32_t* lens, const int32_t* pairs, int64_t count,
+                           void* stream);
+
+/*
+ * Compact the pool.  A page is in use if the table names it as a whole block
+ * of any slot (lens == 0 frees a slot's pages, and so does a shorter length).
+ * The pages in use are moved to ids 0 .. used - 1: one that has such an id
+ * stays, and the others take the free ones in ascending order.  table_out
+ * int32 [slots][max_pages] receives the new table (entries that are no whole
+ * block, or name no page, become -1) and used int32 [1] the number of pages in
+ * use; the cache's own table is only read, and pages in use lie where they lay
+ * before as well, until the caller writes there.  The caller then goes on with
+ * table_out; every page from `used` on is free.
+ * Needs a workspace (wq_kv_paged_compact_workspace_size).
+ */
+wq_status wq_kv_paged_compact(const wq_kv_paged* cache, const int32_t* lens, void* table_out,
+                              int32_t* used, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of wq_kv_paged_compact for this cache. */
+wq_status wq_kv_paged_compact_workspace_size(const wq_kv_paged* cache, size_t* bytes);
+
 /* Static description of a status code. */
 const char* wq_status_string(wq_status s);
 
