@@ -696,9 +696,9 @@ static wq_status check_paged_attention(const wq::PagedArgs& a, int64_t count, in
     if (count < 0 || count > 65535 || q_heads < a.heads || q_heads % a.heads != 0)
         return fail(WQ_ERR_INVALID_ARG, "wq_kv_paged_attention: need 0 <= count <= 65535 and q_heads a multiple of the "
                     "cache's heads (count=%lld q_heads=%lld)", count, q_heads);
-    if (q_heads > 65535 || count * q_heads > (((int64_t)1 << 31) - 1) / (a.max_pages + 4))
-        return fail(WQ_ERR_UNSUPPORTED, "wq_kv_paged_attention: count * q_heads * (max_pages + 4) must be below 2^31 and "
-                    "q_heads below 2^16 (count=%lld q_heads=%lld)", count, q_heads);
+    if (count * q_heads >= ((int64_t)1 << 24) || count * q_heads > (((int64_t)1 << 31) - 1) / (a.max_pages + 4))
+        return fail(WQ_ERR_UNSUPPORTED, "wq_kv_paged_attention: count * q_heads must be below 2^24, and times "
+                    "(max_pages + 4) below 2^31 (count=%lld q_heads=%lld)", count, q_heads);
     return WQ_OK;
 }
 

@@ -516,8 +516,8 @@ wq_status wq_kv_paged_append(const void* k, const void* v, int64_t tokens, int64
  * and where a part ends inside a sequence, its sums are joined by a second
  * kernel through the workspace (wq_kv_paged_workspace_size).  Without a
  * workspace one wavefront walks each sequence and KV head.
- * count <= 65535, count * q_heads * (max_pages + 4) < 2^31
- * (WQ_ERR_UNSUPPORTED).
+ * count <= 65535, count * q_heads < 2^24 and count * q_heads * (max_pages + 4)
+ * < 2^31 (WQ_ERR_UNSUPPORTED otherwise).
  */
 wq_status wq_kv_paged_attention(const void* q, int64_t q_stride, int64_t q_heads,
                                 const wq_kv_paged* cache, const int32_t* lens, const int32_t* seqs,

@@ -97,7 +97,7 @@ def test_append_refusals(kw, want):
 
 @pytest.mark.parametrize("kw,want", [
     (dict(n=-1), BAD), (dict(n=65536), BAD), (dict(n=9, seqs=0), BAD), (dict(qh=0), BAD), (dict(qh=3), BAD),
-    (dict(qh=18, qs=4096, os_=4096), BAD), (dict(qh=65536, qs=1 << 23, os_=1 << 23), UNSUP), (dict(qs=2047), BAD),
+    (dict(qh=18, qs=4096, os_=4096), BAD), (dict(n=256, qh=65536, qs=1 << 23, os_=1 << 23), UNSUP), (dict(qs=2047), BAD),
     (dict(os_=2040), BAD), (dict(qs=2052), MIS), (dict(os_=2050), MIS), (dict(q=FAKE + 8), MIS), (dict(out=FAKE + 4), MIS),
     (dict(q=0), BAD), (dict(out=0), BAD), (dict(lens=0), BAD), (dict(lens=FAKE + 1), MIS), (dict(window=-1), BAD),
     (dict(scale=math.inf), BAD), (dict(scale=math.nan), BAD), (dict(wn=64), BAD), (dict(ws=FAKE + 4, wn=1 << 30), MIS),
