@@ -46,7 +46,7 @@ using namespace paged;
 
 namespace {
 
-typedef unsigned int v4u __attribute__((ext_vector_type(4)));
+typedef unsigned short us2_t __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
@@ -111,6 +111,12 @@ __device__ __forceinline__ h8_t as_h8(const uint4& u) { return __builtin_bit_cas
 struct Masks {
     uint32_t lo, hi;
 };
+// (1024 + c, 64 + c as they come out of the two masks.)
+__device__ __forceinline__ h8_t unpack_raised(uint32_t w, const Masks& k) {
+    const uint32_t s = w >> 8;
+    return as_h8(make_uint4((w & k.lo) | 0x64006400u, (w & k.hi) | 0x54005400u, (s & k.lo) | 0x64006400u,
+                            (s & k.hi) | 0x54005400u));
+}
 __device__ __forceinline__ h8_t unpack(uint32_t w, const Masks& k) {
     const h2_t e = {(_Float16)-1024.0f, (_Float16)-1024.0f}, o = {(_Float16)-64.0f, (_Float16)-64.0f};
     const uint32_t s = w >> 8;
@@ -292,7 +298,7 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
 
     // ---- the row's state.
     uint4 q[4];                           // fp16, in code order
-    float cn = 0.0f;                      // score units (log2) of this lane's column
+    float cn = 0.0f;                      // score units (log2) of this lane's column, >= 0
     float R = 0.0f, L = 0.0f, cz = 0.0f;
     f4_t O[8];
     bool begun = false, bad = false;
@@ -328,15 +334,17 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
                 }
             top = column_max(top);
             const int e = top > 0.0f ? __builtin_amdgcn_frexp_expf(top) - 1 : 0;   // top * 2^-e in [1, 2)
-            cn = __builtin_amdgcn_ldexpf(A.scale, e);
+            // (Within 2^-120 .. 2^100: no product with an infinity is 0 * inf.)
+            cn = __builtin_amdgcn_fmed3f(__builtin_amdgcn_ldexpf(__builtin_fabsf(A.scale), e), 0x1p-120f, 0x1p100f);
+            const float sign = A.scale < 0.0f ? -1.0f : 1.0f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 uint32_t w[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const h2_t v = as_h2(word(raw[j], i));
-                    w[i] = as_u32(h2_t{(_Float16)__builtin_amdgcn_ldexpf((float)v.x, -e),
-                                       (_Float16)__builtin_amdgcn_ldexpf((float)v.y, -e)});
+                    w[i] = as_u32(h2_t{(_Float16)__builtin_amdgcn_ldexpf(sign * (float)v.x, -e),
+                                       (_Float16)__builtin_amdgcn_ldexpf(sign * (float)v.y, -e)});
                 }
                 q[j] = code_order(make_uint4(w[0], w[1], w[2], w[3]));
             }
@@ -365,6 +373,7 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
             __builtin_amdgcn_wave_barrier();
             const uint4* hd = reinterpret_cast<const uint4*>(head_lds) + 4 * g;   // + 16 per header array
             uint4 bh[4], bl[4];
+            const h8_t raised = as_h8(make_uint4(0x64006400u, 0x54005400u, 0x64006400u, 0x54005400u));
             f4_t z4 = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -374,6 +383,8 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
                                    pk_rest(q[j].z, s.z, bh[j].z), pk_rest(q[j].w, s.w, bh[j].w));
                 z4 = mfma(as_h8(z), as_h8(bh[j]), z4);
                 z4 = mfma(as_h8(z), as_h8(bl[j]), z4);
+                z4 = mfma(raised, as_h8(bh[j]), z4);
+                z4 = mfma(raised, as_h8(bl[j]), z4);
             }
             f4_t S[8];
 #pragma unroll
@@ -381,7 +392,7 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
                 S[r] = -z4;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const h8_t a = unpack(word(K[r], j), mk);
+                    const h8_t a = unpack_raised(word(K[r], j), mk);
                     S[r] = mfma(a, as_h8(bh[j]), S[r]);
                     S[r] = mfma(a, as_h8(bl[j]), S[r]);
                 }
@@ -390,32 +401,44 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
             for (int i = 0; i < 8; ++i) K[i] = load16(nbuf, k_off + 256 * i);
             H = load16(nbuf, h_off);
 
-            // Scores in log2 units; tokens left of the window do not count.
-            const int skip = cu.s.left - (cu.s.b0 + cu.unit) * kG - 32 * g;
-            float top = -__builtin_huge_valf();
-            const bool masked = cu.s.left > (cu.s.b0 + cu.unit) * kG;
-#pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                S[r] *= cn;
-                if (masked) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (4 * r + i < skip) S[r][i] = -__builtin_huge_valf();
-                }
-                top = __builtin_fmaxf(top, __builtin_fmaxf(__builtin_fmaxf(S[r][0], S[r][1]),
-                                                           __builtin_fmaxf(S[r][2], S[r][3])));
-            }
             uint4 vs[4], vz[4];
-            h2_t big = h2_t{(_Float16)0.0f, (_Float16)0.0f};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 vs[j] = hd[32 + j];
                 vz[j] = hd[48 + j];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) big = __builtin_elementwise_max(big, as_h2(word(vs[j], i)));
             }
-            const float sm = __builtin_fmaxf((float)big.x, (float)big.y);
-            rebase(top + (float)(__builtin_amdgcn_frexp_expf(sm) - 14));
+            // Tokens left of the window do not count, whatever they hold.
+            const int skip = cu.s.left - (cu.s.b0 + cu.unit) * kG;
+            if (skip > 0) {
+                asm volatile("" ::: "memory");   // (a branch, not selects in every unit)
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (32 * g + 4 * r + i < skip) S[r][i] = -__builtin_huge_valf();
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const auto keep = [&](uint32_t u, int i) {
+                        const int at = 32 * g + 8 * j + 2 * i;
+                        return u & (at < skip ? (at + 1 < skip ? 0u : 0xFFFF0000u) : ~0u);
+                    };
+                    vs[j] = make_uint4(keep(vs[j].x, 0), keep(vs[j].y, 1), keep(vs[j].z, 2), keep(vs[j].w, 3));
+                    vz[j] = make_uint4(keep(vz[j].x, 0), keep(vz[j].y, 1), keep(vz[j].z, 2), keep(vz[j].w, 3));
+                }
+            }
+            float top = S[0][0];
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                top = __builtin_fmaxf(top, __builtin_fmaxf(__builtin_fmaxf(S[r][0], S[r][1]),
+                                                           __builtin_fmaxf(S[r][2], S[r][3])));
+            us2_t big = us2_t{0, 0};          // scales are positive: they order as their bits do
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    big = __builtin_elementwise_max(big, __builtin_bit_cast(us2_t, word(vs[j], i)));
+            const float sm = half_bits_to_float(big.x > big.y ? big.x : big.y);
+            rebase(top * cn + (float)(__builtin_amdgcn_frexp_expf(sm) - 14));
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 // Tokens 32 g + 8 j + 4 e + i.
@@ -424,17 +447,11 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
                 for (int e = 0; e < 2; ++e)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float s2 = S[2 * j + e][i];
-                        const float p = exp2_hw(s2 - R);
+                        const float p = exp2_hw(__builtin_fmaf(S[2 * j + e][i], cn, -R));
                         const h2_t s = as_h2(word(vs[j], 2 * e + (i >> 1))), z = as_h2(word(vz[j], 2 * e + (i >> 1)));
-                        float sv = (float)s[i & 1], zv = (float)z[i & 1];
-                        if (masked) {
-                            sv = s2 == -__builtin_huge_valf() ? 0.0f : sv;
-                            zv = s2 == -__builtin_huge_valf() ? 0.0f : zv;
-                        }
                         L += p;
-                        w[e][i] = p * sv;
-                        cz = __builtin_fmaf(w[e][i], zv, cz);
+                        w[e][i] = p * (float)s[i & 1];
+                        cz = __builtin_fmaf(w[e][i], (float)z[i & 1], cz);
                     }
                 uint32_t wh[4], wl[4];
 #pragma unroll
