@@ -9,28 +9,42 @@
 //
 // Work is cut into units of about 17 KB: one page record (128 tokens of one KV
 // head), or 32 tokens of a window.  The units of all entries stand in one line
-// (entry, KV head and chunk of up to 16 query heads, unit) and the wavefronts
-// of the grid each take an equal run of it, whatever the lengths are: every
-// wave forms the running sum of the units itself from lens.  A wave keeps a
-// running maximum, sum and output per head; where its run covers a whole row
-// (entry, head, chunk) it writes the result, else fp32 partial sums, which a
-// second kernel joins in order.  No atomics: a result depends on the batch,
-// not on timing.
+// (entry, KV head and chunk of up to 16 query heads, unit); the workgroups of
+// the grid (one per compute unit) each take an equal run of it, whatever the
+// lengths are, and their eight waves equal parts of that: every wave forms the
+// running sum of the units itself from lens.  A wave keeps a running maximum,
+// sum and output per head.  Where its part covers a whole row (entry, head,
+// chunk) it writes the result; else the waves' fp32 sums are joined in LDS, in
+// order, and where a row goes past the workgroup, the workgroups' sums by a
+// second kernel.  No atomics: a result depends on the batch, not on timing.
 //
 // One unit of a page, per wave, with lane = 16 g + m:
-//   scores   A = codes of 16 tokens x 32 channels, B = a_d = q_d s_d.  A lane's
-//            16 bytes are channels 32 g .. 32 g + 31 of one token, four
-//            k-steps; row m of token group r is token 32 (m / 4) + 4 r + m % 4,
-//            so that the result's rows 4 g + i of lane (g, head) are tokens
-//            32 g + 4 r + i: what the lane needs as B of the second product.
+//   scores   A = a_d = q_d s_d of 16 slots, B = codes of 16 tokens x 32 channels
+//            (a lane's 16 bytes are channels 32 g .. 32 g + 31 of one token,
+//            four k-steps).  The result's rows 4 g + i are slots, its columns m
+//            tokens, so a lane holds its eight tokens' scores for up to four
+//            slots, and the softmax costs no more than the heads there are.
 //   values   A = codes of 16 channels x 32 tokens (a lane's 16 bytes are tokens
-//            32 g .. of one channel), B = w_t = p_t s_t.
-// Codes become exact fp16 integers (0x6400 | c is 1024 + c, 0x5400 | 16 c is
-// 64 + c; minus that).  a and w are held as fp16 pairs hi + lo (22 bits: hi is
-// the rounded product, lo the rounded rest), two products each, so their
-// rounding stays far below that of the fp16 result.  The zero points enter as
-// sum a_d z_d (a product with the zeros as A, once per unit) and sum w_t z_t
-// (in fp32, per lane).
+//            32 g .. of one channel), B = w_t = p_t s_t of 16 slots, turned
+//            through LDS.
+// a and w are fp16 pairs hi + lo (22 bits: hi is the rounded product, lo the
+// rounded rest), so their rounding stays far below that of the fp16 result.
+// Up to 8 heads a row, hi and lo are neighbouring slots, and every product is
+// issued once; past 8 all slots are heads, and it is issued for hi and for lo.
+// Slot 4 g + i is head g + 4 u, u = i / 2 or i: the kernel is built for NH = 1,
+// 2 or 4 heads a lane (rows of up to 4, 8 and 16).
+//
+// A code needs no conversion: its bits alone, in the low byte of an fp16, are a
+// subnormal number, and the matrix cores take those exactly.  Scores: c 2^-24
+// at even positions and 16 c 2^-24 at odd ones (a shift and four ANDs for a
+// word of eight codes), with q's odd channels 16 times smaller.  Values:
+// 16 c 2^-24 everywhere (two more shifts): the hardware adds products of c
+// 2^-24 to a sum with less of their lower bits (measured over 64 products of
+// positive numbers: 4e-6 off, all one way, against 2.4e-7 for 16 c 2^-24 and
+// for normal numbers), which a score bears (it is at most 1e-5 off) but a long
+// sum of positive weights does not.
+// The zero points enter as sum a_d z_d (a product with the zeros as B, once per
+// unit) and sum w_t z_t (in fp32, per lane).
 //
 // Ranges: q is scaled by a power of two per head so that |q| < 2, hence
 // |a| < 2 * 8736.  w is kept below 2^14 by the reference R of the running
@@ -48,11 +62,14 @@ namespace {
 
 typedef unsigned short us2_t __attribute__((ext_vector_type(2)));
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / 64;
 constexpr int kMaxRow = 16;               // query heads of a row (columns of a product)
 constexpr int kQuarter = 32;              // window tokens of a unit
-constexpr int kVRow = kD + 8;             // fp16 elements of a window row in LDS
+constexpr int kVHalf = kD / 2;            // channels of a window unit's V in LDS at a time
+constexpr int kVRow = kVHalf + 8;         // fp16 elements of such a row
+constexpr int kPart = kD + 4;             // floats of one head's partial sums in LDS: 128 O, R, L
+constexpr int kJoin = 256;                // threads of the joining kernel
 constexpr int kBufWord3 = 0x00020000;     // raw, unswizzled gfx9 buffer
 
 struct AttnArgs {
@@ -65,11 +82,11 @@ struct AttnArgs {
     int count;
     int group;                            // query heads per KV head
     int chunks, per_chunk;                // rows per KV head, query heads of each (the last may have fewer)
-    int workers;                          // waves that share the line; 0: one per row
+    int groups;                           // workgroups that share the line; 0: one wave per row
     float scale;                          // times log2(e)
     int32_t* prefix;                      // [count + 1] units before each entry
-    float2* part_ml;                      // [workers][2][per_chunk] R and sum
-    float* part_o;                        // [workers][2][per_chunk][128]
+    float2* part_ml;                      // [groups][2][per_chunk] R and sum
+    float* part_o;                        // [groups][2][per_chunk][128]
 };
 
 // What of a sequence is read: blocks b0 .. nb - 1 and window quarters w0 ..
@@ -91,6 +108,13 @@ __device__ __forceinline__ Span span_of(int len, int64_t window) {
     return s;
 }
 
+// v, taken anew: what is computed from it is not kept in registers from
+// elsewhere (the loop over units needs nearly all of them).
+__device__ __forceinline__ int anew(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 __device__ __forceinline__ uint32_t pk_mul(uint32_t a, uint32_t b) { return as_u32(as_h2(a) * as_h2(b)); }
@@ -107,26 +131,20 @@ __device__ __forceinline__ uint4 code_order(const uint4& d) {
 
 __device__ __forceinline__ h8_t as_h8(const uint4& u) { return __builtin_bit_cast(h8_t, u); }
 
-// The eight 4-bit codes of a word as fp16 integers, in code order.
-struct Masks {
-    uint32_t lo, hi;
-};
-// (1024 + c, 64 + c as they come out of the two masks.)
-__device__ __forceinline__ h8_t unpack_raised(uint32_t w, const Masks& k) {
+// The eight 4-bit codes of a word, in code order, as fp16.
+constexpr uint32_t kLow = 0x000F000Fu, kHigh = 0x00F000F0u;
+// c 2^-24 at even positions, 16 c 2^-24 at odd ones.
+__device__ __forceinline__ h8_t unpack_k(uint32_t w) {
     const uint32_t s = w >> 8;
-    return as_h8(make_uint4((w & k.lo) | 0x64006400u, (w & k.hi) | 0x54005400u, (s & k.lo) | 0x64006400u,
-                            (s & k.hi) | 0x54005400u));
+    return as_h8(make_uint4(w & kLow, w & kHigh, s & kLow, s & kHigh));
 }
-__device__ __forceinline__ h8_t unpack(uint32_t w, const Masks& k) {
-    const h2_t e = {(_Float16)-1024.0f, (_Float16)-1024.0f}, o = {(_Float16)-64.0f, (_Float16)-64.0f};
-    const uint32_t s = w >> 8;
-    uint4 u;
-    u.x = as_u32(as_h2((w & k.lo) | 0x64006400u) + e);
-    u.y = as_u32(as_h2((w & k.hi) | 0x54005400u) + o);
-    u.z = as_u32(as_h2((s & k.lo) | 0x64006400u) + e);
-    u.w = as_u32(as_h2((s & k.hi) | 0x54005400u) + o);
-    return as_h8(u);
+// 16 c 2^-24.
+__device__ __forceinline__ h8_t unpack_v(uint32_t w) {
+    return as_h8(make_uint4((w << 4) & kHigh, w & kHigh, (w >> 4) & kHigh, (w >> 8) & kHigh));
 }
+constexpr float kKUnit = 0x1p24f, kVUnit = 0x1p20f;   // what scales the sums back
+// fp16 pairs: 2^-24, 2^-20, 1 / 16 and 16.
+constexpr uint32_t kEvenUnit = 0x00010001u, kOddUnit = 0x00100010u, kSixteenth = 0x2C002C00u, kSixteen = 0x4C004C00u;
 
 __device__ __forceinline__ f4_t mfma(const h8_t& a, const h8_t& b, const f4_t& c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
@@ -136,15 +154,29 @@ __device__ __forceinline__ uint32_t word(const uint4& u, int i) { return i == 0 
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// Largest value over the four lanes that share a column.
+// Largest value over the four lanes of an m.
 __device__ __forceinline__ float column_max(float v) {
     v = __builtin_fmaxf(v, __shfl_xor(v, 16, 64));
     return __builtin_fmaxf(v, __shfl_xor(v, 32, 64));
 }
-__device__ __forceinline__ float column_sum(float v) {
-    v += __shfl_xor(v, 16, 64);
-    return v + __shfl_xor(v, 32, 64);
+// Largest value over the 16 lanes of a g.
+__device__ __forceinline__ float row_max(float v) {
+    v = __builtin_fmaxf(v, dpp_f<0xB1>(v));
+    v = __builtin_fmaxf(v, dpp_f<0x4E>(v));
+    v = __builtin_fmaxf(v, dpp_f<0x141>(v));
+    return __builtin_fmaxf(v, dpp_f<0x140>(v));
 }
+
+// n units shared by k takers: the first n % k take one more.
+struct Share {
+    int q, r;
+    __device__ __forceinline__ Share(int n, int k) : q(n / k), r(n - n / k * k) {}
+    __device__ __forceinline__ int begin(int i) const { return i * q + (i < r ? i : r); }
+    __device__ __forceinline__ int of(int f) const {     // whose unit f is (q > 0 or f < r)
+        const int at = r * (q + 1);
+        return f < at ? f / (q + 1) : r + (f - at) / q;
+    }
+};
 
 // 64 entries' slots and lengths, one per lane.
 struct Chunk {
@@ -163,28 +195,47 @@ struct Chunk {
 // A place in the line of units.
 struct Cursor {
     int entry, row, unit;                 // row of the entry, unit of the row
+    int head, first;                      // the row's KV head and first query head of its group
     int slot, units;
     Span s;
     int64_t page;                         // of this unit, if it is a block
     __device__ __forceinline__ bool block() const { return unit < s.nb - s.b0; }
 };
 
+// Bytes of a wave in LDS: a record's headers, the row's queries (64 a lane), and
+// the weights on their way from the scores' lanes to the values' (a window
+// unit's share of them beside 64 channels of its V).
+constexpr int kPRow = kG + 8;             // fp16 elements of a slot's weights
+constexpr int kPWindow = kQuarter + 8;
+constexpr int kTurn = 16 * kPWindow * 2 + kQuarter * kVRow * 2;
+constexpr int kWaveLds = 1024 + 4096 + kTurn;
+static_assert(kTurn >= 16 * kPRow * 2, "a block's weights fit");
+static_assert(kWaveLds >= kMaxRow * kPart * 4, "a wave's last partial sums fit in its place");
+
+template <int NH>
 __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs A) {
-    __shared__ __align__(16) uint16_t lds_head[kWaves][512];             // a record's K and V headers
-    __shared__ __align__(16) uint16_t lds_v[kWaves][kQuarter * kVRow];   // a window unit's V
+    constexpr bool kSplit = NH <= 2;      // hi and lo in slots of their own
+    // [kWaves][kWaveLds], then [kWaves][per_chunk][kPart] first partial sums.
+    extern __shared__ __align__(16) uint8_t lds[];
+    __shared__ int seg_row[2 * kWaves], seg_begin[2 * kWaves], seg_end[2 * kWaves];   // (2 wave + 0 first, 1 last)
     const int lane = threadIdx.x & 63, wv = uniform(threadIdx.x >> 6);
     const int g = lane >> 4, m = lane & 15;
-    const int me = (int)blockIdx.x * kWaves + wv;
     const int rows = (int)A.c.heads * A.chunks;                          // of an entry
-    uint16_t* head_lds = lds_head[wv];
-    uint16_t* v_lds = lds_v[wv];
+    uint16_t* head_lds = reinterpret_cast<uint16_t*>(lds + wv * kWaveLds);
+    uint4* q_lds = reinterpret_cast<uint4*>(lds + wv * kWaveLds + 1024) + lane;   // + 64 j
+    uint16_t* p_lds = head_lds + (1024 + 4096) / 2;
+    uint16_t* v_lds = p_lds + 16 * kPWindow;
+    const bool m_lo = kSplit && (m & 1);  // slot m holds lo halves
+    if (lane < 2) seg_row[2 * wv + lane] = -1;
 
     // ---- this wave's run [f0, f1) of the line, and where it begins.
     Chunk ch;
     Cursor cu;
     int f0, f1;
     cu.unit = 0;
-    if (A.workers == 0) {                 // one wave per row
+    int run0 = 0, run1 = 0;               // the workgroup's run
+    if (A.groups == 0) {                  // one wave per row
+        const int me = (int)blockIdx.x * kWaves + wv;
         if (me >= A.count * rows) return;
         cu.entry = me / rows;
         cu.row = me - cu.entry * rows;
@@ -199,33 +250,36 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
             return;
         }
     } else {
-        int total = 0;
-        for (int at = 0; at < A.count; at += 64) {
+        int total = 0, u = 0, inc = 0;
+        const auto scan = [&](int at) {   // units of 64 entries, and their running sum
             ch.load(A, at, lane);
-            int u = span_of(ch.len, A.window).units() * rows, inc = u;
+            u = inc = span_of(ch.len, A.window).units() * rows;
 #pragma unroll
             for (int o = 1; o < 64; o <<= 1) {
                 const int up = __shfl_up(inc, o, 64);
                 if (lane >= o) inc += up;
             }
-            if (me == 0 && at + lane < A.count) A.prefix[at + lane] = total + inc - u;
+        };
+        const bool note = blockIdx.x == 0 && wv == 0;
+        for (int at = 0; at < A.count; at += 64) {
+            scan(at);
+            if (note && at + lane < A.count) A.prefix[at + lane] = total + inc - u;
             total += __builtin_amdgcn_readlane(inc, 63);
         }
-        if (me == 0 && lane == 0) A.prefix[A.count] = total;
-        const int W = A.workers < total ? A.workers : total;
-        if (me >= W) return;
-        f0 = (int)((int64_t)me * total / W);
-        f1 = (int)((int64_t)(me + 1) * total / W);
+        if (note && lane == 0) A.prefix[A.count] = total;
+        const int used = A.groups < total ? A.groups : total;
+        if ((int)blockIdx.x >= used) return;
+        const Share share(total, used);
+        run0 = share.begin(blockIdx.x);
+        run1 = share.begin(blockIdx.x + 1);
+        const int n = run1 - run0;
+        f0 = run0 + (int)((int64_t)n * wv / kWaves);
+        f1 = run0 + (int)((int64_t)n * (wv + 1) / kWaves);
+        const int find = f0 < f1 ? f0 : run0;            // (a wave without units looks at any)
         int before = 0;
-        for (int at = 0;; at += 64) {     // ends: f0 < total
-            if (A.count > 64) ch.load(A, at, lane);
-            int u = span_of(ch.len, A.window).units() * rows, inc = u;
-#pragma unroll
-            for (int o = 1; o < 64; o <<= 1) {
-                const int up = __shfl_up(inc, o, 64);
-                if (lane >= o) inc += up;
-            }
-            const uint64_t past = __builtin_amdgcn_ballot_w64(before + inc > f0);
+        for (int at = 0;; at += 64) {     // ends: find < total
+            if (A.count > 64) scan(at);
+            const uint64_t past = __builtin_amdgcn_ballot_w64(before + inc > find);
             if (past != 0) {
                 const int i = __builtin_ctzll(past);
                 before += __builtin_amdgcn_readlane(inc - u, i);
@@ -234,16 +288,18 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
             }
             before += __builtin_amdgcn_readlane(inc, 63);
         }
-        cu.unit = f0 - before;            // in the entry, for now
+        cu.unit = find - before;          // in the entry, for now
     }
     cu.entry = uniform(cu.entry);
     cu.slot = __builtin_amdgcn_readlane(ch.slot, cu.entry & 63);
     cu.s = span_of(__builtin_amdgcn_readlane(ch.len, cu.entry & 63), A.window);
     cu.units = cu.s.units();
-    if (A.workers != 0) {
+    if (A.groups != 0) {
         cu.row = cu.unit / cu.units;
         cu.unit -= cu.row * cu.units;
     }
+    cu.head = cu.row / A.chunks;
+    cu.first = (cu.row - cu.head * A.chunks) * A.per_chunk;
 
     const auto fetch_page = [&](Cursor& c) {
         c.page = c.block() ? (int64_t)A.c.table[c.slot * A.c.max_pages + c.s.b0 + c.unit] : 0;
@@ -251,8 +307,14 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
     const auto advance = [&](Cursor& c) {   // to the next unit of the line (there is one)
         if (++c.unit < c.units) return;
         c.unit = 0;
+        c.first += A.per_chunk;
+        if (c.first >= A.group) {
+            c.first = 0;
+            ++c.head;
+        }
         if (++c.row < rows) return;
         c.row = 0;
+        c.head = 0;
         do {
             if ((++c.entry & 63) == 0) ch.load(A, c.entry, lane);
             c.slot = __builtin_amdgcn_readlane(ch.slot, c.entry & 63);
@@ -263,32 +325,55 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
 
     // ---- loads of a block's record: through a buffer of its bytes, or of none
     // where there is no such block, so that the loads are always issued.
-    const uint32_t k_off = (uint32_t)((32 * (m >> 2) + (m & 3)) * kRow + 16 * g);   // + 256 per token group
+    const uint32_t k_off = (uint32_t)((8 * m) * kRow + 16 * g);                     // + 64 per token of the lane's eight
     const uint32_t v_off = (uint32_t)(kVCodes + m * kRow + 16 * g);                 // + 1024 per 16 channels
     const uint32_t h_off = (uint32_t)(kKScales + 16 * lane);
     const auto buffer = [&](const Cursor& c, bool valid) {
         const int64_t page = c.page >= 0 && c.page < A.c.num_pages ? c.page : 0;
-        const uint8_t* rec = record(A.c, page, c.row / A.chunks);
+        const uint8_t* rec = record(A.c, page, c.head);
         return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(rec), (short)0, valid && c.block() ? kRecord : 0,
                                                  kBufWord3);
     };
     const auto load16 = [&](__amdgpu_buffer_rsrc_t r, uint32_t off) {
         return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 2));   // 2: streamed
     };
+    // (Offsets taken anew, so that the constants stay in the instructions.)
+    const auto load_k = [&](__amdgpu_buffer_rsrc_t r, uint4 (&K)[8], uint4& H) {
+        const uint32_t ko = (uint32_t)anew((int)k_off);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) K[i] = load16(r, ko + kRow * (i / 2 + 4 * (i & 1)));
+        H = load16(r, (uint32_t)anew((int)h_off));
+    };
+    const auto load_v = [&](__amdgpu_buffer_rsrc_t r, uint4 (&V)[8]) {
+        const uint32_t vo = (uint32_t)anew((int)v_off);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) V[i] = load16(r, vo + 1024 * i);
+    };
 
-    Masks mk;
-    mk.lo = vgpr_const(0x000F000Fu);
-    mk.hi = vgpr_const(0x00F000F0u);
+    const float zero = __builtin_bit_cast(float, vgpr_const(0));
 
-    uint4 K[8], V[8], H;
+    // A row's queries as they lie: 32 channels of this lane's head.
+    const auto load_q = [&](const Cursor& c, uint4 (&raw)[4]) {
+        const int n = A.group - c.first < A.per_chunk ? A.group - c.first : A.per_chunk;
+        const int mq = anew(m), gq = anew(g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) raw[j] = make_uint4(0, 0, 0, 0);
+        const int hq = (mq >> 2) + 4 * (kSplit ? (mq & 3) >> 1 : mq & 3);
+        if (hq < n && (NH > 1 || (mq & 3) < 2)) {
+            const uint4* src = reinterpret_cast<const uint4*>(A.q + c.entry * A.q_stride +
+                                                              (int64_t)(c.head * A.group + c.first + hq) * kD + 32 * gq);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) raw[j] = src[j];
+        }
+    };
+
+    uint4 K[8], V[8], H, raw0[4];
+    load_q(cu, raw0);
     fetch_page(cu);
     {
-        const auto r = buffer(cu, true);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) K[i] = load16(r, k_off + 256 * i);
-        H = load16(r, h_off);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) V[i] = load16(r, v_off + 1024 * i);
+        const auto r = buffer(cu, f0 < f1);
+        load_k(r, K, H);
+        load_v(r, V);
     }
     Cursor nx = cu;
     if (f1 - f0 > 1) {
@@ -297,72 +382,143 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
     }
 
     // ---- the row's state.
-    uint4 q[4];                           // fp16, in code order
-    float cn = 0.0f;                      // score units (log2) of this lane's column, >= 0
-    float R = 0.0f, L = 0.0f, cz = 0.0f;
-    f4_t O[8];
-    bool begun = false, bad = false;
+    // Of the lane's heads g + 4 u, alike in the lanes of a g (L and cz: in
+    // their sum): score units (log2, >= 0), reference, sum of weights, zeros.
+    float cn[NH], R[NH], L[NH], cz[NH];
+    f4_t O[8] = {};                       // / 2^20 while the row is in its blocks
+    bool bad = false, in_blocks = false;
     int heads_here = 0;                   // query heads of the row
 
-    for (int f = f0; f < f1; ++f) {
-        const int h = cu.row / A.chunks, first = (cu.row - h * A.chunks) * A.per_chunk;
-        if (!begun) {
-            begun = true;
-            bad = false;
-            heads_here = A.group - first < A.per_chunk ? A.group - first : A.per_chunk;
-            R = -__builtin_huge_valf();
-            L = 0.0f;
-            cz = 0.0f;
+    // A new row, from its queries: |q| < 2 by a power of two that cn undoes.
+    const auto start_row = [&](const Cursor& c, const uint4 (&raw)[4]) {
+        bad = false;
+        in_blocks = true;
+        heads_here = A.group - c.first < A.per_chunk ? A.group - c.first : A.per_chunk;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) O[i] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
-            uint4 raw[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) raw[j] = make_uint4(0, 0, 0, 0);
-            if (m < heads_here) {
-                const uint4* src = reinterpret_cast<const uint4*>(A.q + cu.entry * A.q_stride +
-                                                                  (int64_t)(h * A.group + first + m) * kD + 32 * g);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) raw[j] = src[j];
-            }
-            float top = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const h2_t v = as_h2(word(raw[j], i));
-                    top = __builtin_fmaxf(top, __builtin_fmaxf(__builtin_fabsf((float)v.x), __builtin_fabsf((float)v.y)));
-                }
-            top = column_max(top);
-            const int e = top > 0.0f ? __builtin_amdgcn_frexp_expf(top) - 1 : 0;   // top * 2^-e in [1, 2)
-            // (Within 2^-120 .. 2^100: no product with an infinity is 0 * inf.)
-            cn = __builtin_amdgcn_fmed3f(__builtin_amdgcn_ldexpf(__builtin_fabsf(A.scale), e), 0x1p-120f, 0x1p100f);
-            const float sign = A.scale < 0.0f ? -1.0f : 1.0f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t w[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const h2_t v = as_h2(word(raw[j], i));
-                    w[i] = as_u32(h2_t{(_Float16)__builtin_amdgcn_ldexpf(sign * (float)v.x, -e),
-                                       (_Float16)__builtin_amdgcn_ldexpf(sign * (float)v.y, -e)});
-                }
-                q[j] = code_order(make_uint4(w[0], w[1], w[2], w[3]));
-            }
+        for (int u = 0; u < NH; ++u) {
+            R[u] = -__builtin_huge_valf();
+            L[u] = cz[u] = 0.0f;
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) O[i] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        float top = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const h2_t v = as_h2(word(raw[j], i));
+                top = __builtin_fmaxf(top, __builtin_fmaxf(__builtin_fabsf((float)v.x), __builtin_fabsf((float)v.y)));
+            }
+        top = column_max(top);
+        const int e = top > 0.0f ? __builtin_amdgcn_frexp_expf(top) - 1 : 0;   // top * 2^-e in [1, 2)
+        // (Within 2^-120 .. 2^80: no product with an infinity is 0 * inf.)
+        const float unit = __builtin_amdgcn_fmed3f(__builtin_amdgcn_ldexpf(__builtin_fabsf(A.scale), e), 0x1p-120f, 0x1p80f);
+#pragma unroll
+        for (int u = 0; u < NH; ++u) cn[u] = __shfl(unit, 4 * g + (kSplit ? 2 * u : u), 64);   // from the head's slot
+        const float sign = A.scale < 0.0f ? -1.0f : 1.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const h2_t v = as_h2(word(raw[j], i));
+                w[i] = as_u32(h2_t{(_Float16)__builtin_amdgcn_ldexpf(sign * (float)v.x, -e),
+                                   (_Float16)__builtin_amdgcn_ldexpf(sign * (float)v.y, -e)});
+            }
+            // To LDS (16 registers), in code order, the odd channels / 16.
+            const uint4 c4 = code_order(make_uint4(w[0], w[1], w[2], w[3]));
+            q_lds[64 * j] = make_uint4(c4.x, pk_mul(c4.y, kSixteenth), c4.z, pk_mul(c4.w, kSixteenth));
+        }
+    };
+    start_row(cu, raw0);
+
+    // What the lanes of head g + 4 u hold, for the lanes of a slot m of it.
+    const auto to_slot = [&](const float (&v)[NH]) {
+        const int mt = anew(m), from = 16 * (mt >> 2), u_of = kSplit ? (mt & 3) >> 1 : mt & 3;
+        float r = __shfl(v[0], from, 64);
+#pragma unroll
+        for (int u = 1; u < NH; ++u) {
+            const float w = __shfl(v[u], from, 64);
+            r = u_of == u ? w : r;
+        }
+        return r;
+    };
+    // A row's sums as they are (in both of a head's slots): all tokens together,
+    // the zero points taken out.
+    const auto settle = [&](float& l) {
+        float ls[NH], zs[NH];
+#pragma unroll
+        for (int u = 0; u < NH; ++u) {
+            ls[u] = group_sum<16>(L[u]);
+            zs[u] = group_sum<16>(cz[u]);
+        }
+        const float z = to_slot(zs);
+        l = bad ? __builtin_nanf("") : to_slot(ls);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+            if (in_blocks) O[t] *= kVUnit;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) O[t][i] = (kSplit ? O[t][i] + dpp_f<0xB1>(O[t][i]) : O[t][i]) - z;
+        }
+    };
+    // The head (of the row) that this lane writes sums of, or -1.
+    const auto my_head = [&]() {
+        const int mt = anew(m), h = (mt >> 2) + 4 * (kSplit ? (mt & 3) >> 1 : mt & 3);
+        return h < heads_here && !(kSplit && (mt & 1)) && (NH > 1 || (mt & 3) < 2) ? h : -1;
+    };
+    const auto keep = [&](float* part, float l) {   // partial sums to LDS
+        const float r = to_slot(R);
+        const int h = my_head(), gp = anew(g);
+        if (h < 0) return;
+#pragma unroll
+        for (int t = 0; t < 8; ++t) *reinterpret_cast<f4_t*>(part + h * kPart + 16 * t + 4 * gp) = O[t];
+        if (gp == 0) *reinterpret_cast<float2*>(part + h * kPart + kD) = make_float2(r, l);
+    };
+    const auto note_segment = [&](int at, int f) {
+        if (lane == 0) {
+            seg_row[at] = cu.entry * rows + cu.row;
+            seg_begin[at] = f - cu.unit;
+            seg_end[at] = f - cu.unit + cu.units;
+        }
+    };
+    bool open = false;                    // a row left unfinished (or finished, but begun before) at the end
+
+    for (int f = f0; f < f1; ++f) {
         const bool more = f + 1 < f1;
         const auto nbuf = buffer(nx, more);
 
         // New reference for the running exponent, and what is held with the old one.
-        const auto rebase = [&](float cand) {
-            const float Rn = __builtin_fmaxf(R, column_max(cand));
-            if (__builtin_amdgcn_ballot_w64(Rn > R) != 0) {
-                const float alpha = exp2_hw(R - Rn);
-                L *= alpha;
-                cz *= alpha;
+        const auto rebase = [&](const float (&cand)[NH]) {
+            float alpha[NH];
+            bool grows = false;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) O[i] *= alpha;
-                R = Rn;
+            for (int u = 0; u < NH; ++u) {
+                const float r = __builtin_fmaxf(R[u], row_max(cand[u]));
+                grows |= r > R[u];
+                alpha[u] = R[u] - r;
+                R[u] = r;
             }
+            if (__builtin_amdgcn_ballot_w64(grows) != 0) {
+#pragma unroll
+                for (int u = 0; u < NH; ++u) {
+                    alpha[u] = exp2_hw(alpha[u]);
+                    L[u] *= alpha[u];
+                    cz[u] *= alpha[u];
+                }
+                const float a = to_slot(alpha);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) O[i] *= a;
+            }
+        };
+        // Weights hi + lo of head u into their slots' rows.
+        const auto halves = [](float w0, float w1, uint32_t& hi, uint32_t& lo) {
+            const h2_t h = h2_t{(_Float16)w0, (_Float16)w1};
+            hi = as_u32(h);
+            lo = as_u32(h2_t{(_Float16)(w0 - (float)h.x), (_Float16)(w1 - (float)h.y)});
+        };
+        const auto turned = [&]() {           // the wave's LDS writes before its reads that follow
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
         };
 
         if (cu.block()) {
@@ -372,218 +528,328 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
             __builtin_amdgcn_wave_barrier();
             const uint4* hd = reinterpret_cast<const uint4*>(head_lds) + 4 * g;   // + 16 per header array
-            uint4 bh[4], bl[4];
-            const h8_t raised = as_h8(make_uint4(0x64006400u, 0x54005400u, 0x64006400u, 0x54005400u));
+            uint4 a0[4], a1[4];               // hi or lo (a0); hi and lo past 8 heads
             f4_t z4 = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const uint4 s = code_order(hd[j]), z = code_order(hd[16 + j]);
-                bh[j] = make_uint4(pk_mul(q[j].x, s.x), pk_mul(q[j].y, s.y), pk_mul(q[j].z, s.z), pk_mul(q[j].w, s.w));
-                bl[j] = make_uint4(pk_rest(q[j].x, s.x, bh[j].x), pk_rest(q[j].y, s.y, bh[j].y),
-                                   pk_rest(q[j].z, s.z, bh[j].z), pk_rest(q[j].w, s.w, bh[j].w));
-                z4 = mfma(as_h8(z), as_h8(bh[j]), z4);
-                z4 = mfma(as_h8(z), as_h8(bl[j]), z4);
-                z4 = mfma(raised, as_h8(bh[j]), z4);
-                z4 = mfma(raised, as_h8(bl[j]), z4);
+                const uint4 s = code_order(hd[j]), qj = q_lds[64 * j];
+                uint4 z = code_order(hd[16 + j]);       // in the codes' units (exact: at most 11 bits, above 2^-24)
+                z = make_uint4(pk_mul(z.x, kEvenUnit), pk_mul(z.y, kOddUnit), pk_mul(z.z, kEvenUnit), pk_mul(z.w, kOddUnit));
+                a0[j] = make_uint4(pk_mul(qj.x, s.x), pk_mul(qj.y, s.y), pk_mul(qj.z, s.z), pk_mul(qj.w, s.w));
+                a1[j] = make_uint4(pk_rest(qj.x, s.x, a0[j].x), pk_rest(qj.y, s.y, a0[j].y),
+                                   pk_rest(qj.z, s.z, a0[j].z), pk_rest(qj.w, s.w, a0[j].w));
+                if (kSplit)
+                    a0[j] = make_uint4(m_lo ? a1[j].x : a0[j].x, m_lo ? a1[j].y : a0[j].y, m_lo ? a1[j].z : a0[j].z,
+                                       m_lo ? a1[j].w : a0[j].w);
+                z4 = mfma(as_h8(a0[j]), as_h8(z), z4);
+                if (!kSplit) z4 = mfma(as_h8(a1[j]), as_h8(z), z4);
             }
             f4_t S[8];
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                S[r] = -z4;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const h8_t a = unpack_raised(word(K[r], j), mk);
-                    S[r] = mfma(a, as_h8(bh[j]), S[r]);
-                    S[r] = mfma(a, as_h8(bl[j]), S[r]);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) K[i] = load16(nbuf, k_off + 256 * i);
-            H = load16(nbuf, h_off);
-
-            uint4 vs[4], vz[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                vs[j] = hd[32 + j];
-                vz[j] = hd[48 + j];
-            }
-            // Tokens left of the window do not count, whatever they hold.
-            const int skip = cu.s.left - (cu.s.b0 + cu.unit) * kG;
-            if (skip > 0) {
-                asm volatile("" ::: "memory");   // (a branch, not selects in every unit)
-#pragma unroll
-                for (int r = 0; r < 8; ++r)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (32 * g + 4 * r + i < skip) S[r][i] = -__builtin_huge_valf();
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const auto keep = [&](uint32_t u, int i) {
-                        const int at = 32 * g + 8 * j + 2 * i;
-                        return u & (at < skip ? (at + 1 < skip ? 0u : 0xFFFF0000u) : ~0u);
-                    };
-                    vs[j] = make_uint4(keep(vs[j].x, 0), keep(vs[j].y, 1), keep(vs[j].z, 2), keep(vs[j].w, 3));
-                    vz[j] = make_uint4(keep(vz[j].x, 0), keep(vz[j].y, 1), keep(vz[j].z, 2), keep(vz[j].w, 3));
-                }
-            }
-            float top = S[0][0];
-#pragma unroll
-            for (int r = 0; r < 8; ++r)
-                top = __builtin_fmaxf(top, __builtin_fmaxf(__builtin_fmaxf(S[r][0], S[r][1]),
-                                                           __builtin_fmaxf(S[r][2], S[r][3])));
-            us2_t big = us2_t{0, 0};          // scales are positive: they order as their bits do
+            for (int r = 0; r < 8; ++r) S[r] = -z4;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    big = __builtin_elementwise_max(big, __builtin_bit_cast(us2_t, word(vs[j], i)));
-            const float sm = half_bits_to_float(big.x > big.y ? big.x : big.y);
-            rebase(top * cn + (float)(__builtin_amdgcn_frexp_expf(sm) - 14));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                // Tokens 32 g + 8 j + 4 e + i.
-                float w[2][4];
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float p = exp2_hw(__builtin_fmaf(S[2 * j + e][i], cn, -R));
-                        const h2_t s = as_h2(word(vs[j], 2 * e + (i >> 1))), z = as_h2(word(vz[j], 2 * e + (i >> 1)));
-                        L += p;
-                        w[e][i] = p * (float)s[i & 1];
-                        cz = __builtin_fmaf(w[e][i], (float)z[i & 1], cz);
-                    }
-                uint32_t wh[4], wl[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const h2_t hi = h2_t{(_Float16)w[0][i], (_Float16)w[1][i]};
-                    wh[i] = as_u32(hi);
-                    wl[i] = as_u32(h2_t{(_Float16)(w[0][i] - (float)hi.x), (_Float16)(w[1][i] - (float)hi.y)});
+                for (int r = 0; r < 8; ++r) {
+                    const h8_t b = unpack_k(word(K[r], j));
+                    S[r] = mfma(as_h8(a0[j]), b, S[r]);
+                    if (!kSplit) S[r] = mfma(as_h8(a1[j]), b, S[r]);
                 }
-                const h8_t b0 = as_h8(make_uint4(wh[0], wh[1], wh[2], wh[3]));
-                const h8_t b1 = as_h8(make_uint4(wl[0], wl[1], wl[2], wl[3]));
+            load_k(nbuf, K, H);
+
+            // Scores of the lane's tokens 8 m + place(r) for its heads.
+            float sc[NH][8];
+#pragma unroll
+            for (int u = 0; u < NH; ++u)
+#pragma unroll
+                for (int r = 0; r < 8; ++r) sc[u][r] = kSplit ? S[r][(2 * u) & 3] + S[r][(2 * u + 1) & 3] : S[r][u];
+            // Tokens left of the window do not count, whatever they hold.
+            const int skip = cu.s.left - (cu.s.b0 + cu.unit) * kG;
+            if (skip > 0) {
+                const int ms = anew(m), two = 2 * anew(lane);
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+#pragma unroll
+                    for (int u = 0; u < NH; ++u)
+                        if (8 * ms + r / 2 + 4 * (r & 1) < skip) sc[u][r] = -__builtin_huge_valf();
+                uint32_t* v = reinterpret_cast<uint32_t*>(head_lds) + 128 + two / 2;   // this lane's two tokens
+                const uint32_t kept = two < skip ? (two + 1 < skip ? 0u : 0xFFFF0000u) : ~0u;
+                v[0] &= kept;
+                v[64] &= kept;
+                turned();
+            }
+            const uint4 vs = reinterpret_cast<const uint4*>(head_lds)[32 + m];
+            const uint4 vz = reinterpret_cast<const uint4*>(head_lds)[48 + m];
+            us2_t big = us2_t{0, 0};          // scales are positive: they order as their bits do
+#pragma unroll
+            for (int i = 0; i < 4; ++i) big = __builtin_elementwise_max(big, __builtin_bit_cast(us2_t, word(vs, i)));
+            const float above = (float)(__builtin_amdgcn_frexp_expf(half_bits_to_float(big.x > big.y ? big.x : big.y)) - 14);
+            float cand[NH];
+#pragma unroll
+            for (int u = 0; u < NH; ++u) {
+                float top = sc[u][0];
+#pragma unroll
+                for (int r = 1; r < 8; ++r) top = __builtin_fmaxf(top, sc[u][r]);
+                cand[u] = __builtin_fmaf(top, cn[u] * kKUnit, above);
+            }
+            rebase(cand);
+            uint4 low[NH];
+#pragma unroll
+            for (int u = 0; u < NH; ++u) {
+                const float cc = cn[u] * kKUnit;
+                float w[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    const int e = r / 2 + 4 * (r & 1);
+                    const float p = exp2_hw(__builtin_fmaf(sc[u][r], cc, -R[u]));
+                    L[u] += p;
+                    w[r] = __builtin_fmaf(p, (float)as_h2(word(vs, e >> 1))[e & 1], zero);   // (one v_fma_mix)
+                    cz[u] = __builtin_fmaf(w[r], (float)as_h2(word(vz, e >> 1))[e & 1], cz[u]);
+                }
+                uint4 high;
+                halves(w[0], w[1], high.x, low[u].x);
+                halves(w[2], w[3], high.y, low[u].y);
+                halves(w[4], w[5], high.z, low[u].z);
+                halves(w[6], w[7], high.w, low[u].w);
+                uint4* to = reinterpret_cast<uint4*>(p_lds + (4 * g + (kSplit ? 2 * u : u)) * kPRow + 8 * m);
+                *to = high;
+                if (kSplit) *reinterpret_cast<uint4*>(p_lds + (4 * g + 2 * u + 1) * kPRow + 8 * m) = low[u];
+            }
+            turned();
+            uint4 b0[4], b1[4];
+            const uint4* pr = reinterpret_cast<const uint4*>(p_lds + m * kPRow + 32 * g);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) b0[j] = pr[j];
+            if (!kSplit) {                    // the lo halves through the same rows
+                turned();
+#pragma unroll
+                for (int u = 0; u < NH; ++u)
+                    *reinterpret_cast<uint4*>(p_lds + (4 * g + u) * kPRow + 8 * m) = low[u];
+                turned();
+#pragma unroll
+                for (int j = 0; j < 4; ++j) b1[j] = pr[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int t = 0; t < 8; ++t) {
-                    const h8_t a = unpack(word(V[t], j), mk);
-                    O[t] = mfma(a, b0, O[t]);
-                    O[t] = mfma(a, b1, O[t]);
+                    const h8_t c = unpack_v(word(V[t], j));
+                    O[t] = mfma(c, as_h8(b0[j]), O[t]);
+                    if (!kSplit) O[t] = mfma(c, as_h8(b1[j]), O[t]);
                 }
-            }
-            __builtin_amdgcn_wave_barrier();   // the headers are read before the next unit's go in
+            __builtin_amdgcn_wave_barrier();   // what is in LDS is read before the next unit's goes in
         } else {
             // ---- 32 tokens of the window, fp16.
+            const int gw = anew(g), mw = anew(m);
             const int t0 = kQuarter * (cu.s.w0 + cu.unit - (cu.s.nb - cu.s.b0));
             const int end = cu.s.len - cu.s.nb * kG, begin = cu.s.left - cu.s.nb * kG;   // rows that count
-            const uint16_t* wk = window_of(A.c, cu.slot, h, 0) + t0 * kD;
-            const uint16_t* wvp = window_of(A.c, cu.slot, h, 1) + t0 * kD;
+            const uint16_t* wk = window_of(A.c, cu.slot, cu.head, 0) + t0 * kD;
+            const uint16_t* wvp = window_of(A.c, cu.slot, cu.head, 1) + t0 * kD;
             uint4 kx[2][4], vx[8];
 #pragma unroll
             for (int r = 0; r < 2; ++r)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    kx[r][j] = *reinterpret_cast<const uint4*>(wk + (8 * (m >> 2) + 4 * r + (m & 3)) * kD + 32 * g + 8 * j);
+                    kx[r][j] = *reinterpret_cast<const uint4*>(wk + (16 * r + mw) * kD + 32 * gw + 8 * j);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) vx[i] = *reinterpret_cast<const uint4*>(wvp + (4 * i + g) * kD + 8 * m);
-            f4_t S[2];
-            float top = -__builtin_huge_valf();
+            for (int i = 0; i < 8; ++i) vx[i] = *reinterpret_cast<const uint4*>(wvp + (4 * i + gw) * kD + 8 * mw);
+            if (in_blocks) {
+                in_blocks = false;
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                S[r] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+                for (int t = 0; t < 8; ++t) O[t] *= kVUnit;
+            }
+            f4_t S[2] = {};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) S[r] = mfma(as_h8(code_order(kx[r][j])), as_h8(q[j]), S[r]);
+            for (int j = 0; j < 4; ++j) {
+                const uint4 c4 = q_lds[64 * j];    // (exact: the lo slots hold nothing)
+                const uint4 qw = m_lo ? make_uint4(0, 0, 0, 0)
+                                      : make_uint4(c4.x, pk_mul(c4.y, kSixteen), c4.z, pk_mul(c4.w, kSixteen));
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int t = t0 + 8 * g + 4 * r + i;
-                    S[r][i] = t >= begin && t < end ? S[r][i] * cn : -__builtin_huge_valf();
-                    top = __builtin_fmaxf(top, S[r][i]);
+                for (int r = 0; r < 2; ++r) S[r] = mfma(as_h8(qw), as_h8(code_order(kx[r][j])), S[r]);
+            }
+            float sc[NH][2], cand[NH];
+#pragma unroll
+            for (int u = 0; u < NH; ++u) {
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int t = t0 + 16 * r + mw;
+                    sc[u][r] = t >= begin && t < end ? S[r][kSplit ? (2 * u) & 3 : u] * cn[u] : -__builtin_huge_valf();
+                }
+                cand[u] = __builtin_fmaxf(sc[u][0], sc[u][1]) + (float)(1 - 14);
+            }
+            rebase(cand);
+            uint32_t low[NH];
+#pragma unroll
+            for (int u = 0; u < NH; ++u) {
+                const float p0 = exp2_hw(sc[u][0] - R[u]), p1 = exp2_hw(sc[u][1] - R[u]);
+                L[u] += p0 + p1;
+                uint32_t high;
+                halves(p0, p1, high, low[u]);
+                uint16_t* to = p_lds + (4 * gw + (kSplit ? 2 * u : u)) * kPWindow + mw;
+                to[0] = (uint16_t)high;
+                to[16] = (uint16_t)(high >> 16);
+                if (kSplit) {
+                    to[kPWindow] = (uint16_t)low[u];
+                    to[kPWindow + 16] = (uint16_t)(low[u] >> 16);
                 }
             }
-            // V rows to LDS (zeros where a row does not count: it may hold
-            // anything), to be read by channel.
+            turned();
+            const uint4* pr = reinterpret_cast<const uint4*>(p_lds + mw * kPWindow + 8 * gw);
+            const h8_t b0 = as_h8(*pr);
+            h8_t b1 = b0;
+            if (!kSplit) {
+                turned();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int t = t0 + 4 * i + g;
-                const bool in = t >= begin && t < end;
-                *reinterpret_cast<uint4*>(v_lds + (4 * i + g) * kVRow + 8 * m) =
-                    in ? vx[i] : make_uint4(0, 0, 0, 0);
-            }
-            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-            rebase(top + (float)(1 - 14));
-            uint32_t wh[4], wl[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float p0 = exp2_hw(S[i >> 1][2 * (i & 1)] - R), p1 = exp2_hw(S[i >> 1][2 * (i & 1) + 1] - R);
-                L += p0 + p1;
-                const h2_t hi = h2_t{(_Float16)p0, (_Float16)p1};
-                wh[i] = as_u32(hi);
-                wl[i] = as_u32(h2_t{(_Float16)(p0 - (float)hi.x), (_Float16)(p1 - (float)hi.y)});
-            }
-            const h8_t b0 = as_h8(make_uint4(wh[0], wh[1], wh[2], wh[3]));
-            const h8_t b1 = as_h8(make_uint4(wl[0], wl[1], wl[2], wl[3]));
-#pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                uint32_t u[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint16_t* at = v_lds + (8 * g + 2 * i) * kVRow + 16 * t + m;
-                    u[i] = (uint32_t)at[0] | ((uint32_t)at[kVRow] << 16);
+                for (int u = 0; u < NH; ++u) {
+                    uint16_t* to = p_lds + (4 * gw + u) * kPWindow + mw;
+                    to[0] = (uint16_t)low[u];
+                    to[16] = (uint16_t)(low[u] >> 16);
                 }
-                const h8_t a = as_h8(make_uint4(u[0], u[1], u[2], u[3]));
-                O[t] = mfma(a, b0, O[t]);
-                O[t] = mfma(a, b1, O[t]);
+                turned();
+                b1 = as_h8(*pr);
+            }
+            // V rows through LDS, 64 channels at a time, to be read by channel
+            // (zeros where a row does not count: it may hold anything).
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int t = t0 + 4 * i + gw;
+                    const bool in = t >= begin && t < end;
+                    if ((mw >> 3) == half)
+                        *reinterpret_cast<uint4*>(v_lds + (4 * i + gw) * kVRow + 8 * (mw & 7)) =
+                            in ? vx[i] : make_uint4(0, 0, 0, 0);
+                }
+                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    uint32_t u[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint16_t* at = v_lds + (8 * gw + 2 * i) * kVRow + 16 * t + mw;
+                        u[i] = (uint32_t)at[0] | ((uint32_t)at[kVRow] << 16);
+                    }
+                    const h8_t a = as_h8(make_uint4(u[0], u[1], u[2], u[3]));
+                    O[4 * half + t] = mfma(a, b0, O[4 * half + t]);
+                    if (!kSplit) O[4 * half + t] = mfma(a, b1, O[4 * half + t]);
+                }
+                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
             }
             __builtin_amdgcn_wave_barrier();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) K[i] = load16(nbuf, k_off + 256 * i);
-            H = load16(nbuf, h_off);
+            load_k(nbuf, K, H);
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) V[i] = load16(nbuf, v_off + 1024 * i);
+        load_v(nbuf, V);
 
         // ---- the end of the row, or of this wave's part of it.
         if (!more || cu.unit + 1 == cu.units) {
-            begun = false;
-            const int from = cu.unit - (f - f0);           // the row's unit at f0 (below 0: it began later)
-            const bool whole = from <= 0 && cu.unit + 1 == cu.units;
-            const float l = bad ? __builtin_nanf("") : column_sum(L), z = column_sum(cz);
-            if (whole) {
+            if (cu.unit <= f - f0 && cu.unit + 1 == cu.units) {   // all of the row was here
+                float l;
+                settle(l);
                 const float inv = 1.0f / l;
-                uint16_t* o = A.out + cu.entry * A.out_stride + (int64_t)(h * A.group + first + m) * kD + 4 * g;
-                if (m < heads_here) {
+                const int mo = my_head();
+                uint16_t* o = A.out + cu.entry * A.out_stride + (int64_t)(cu.head * A.group + cu.first + mo) * kD + 4 * anew(g);
+                if (mo >= 0) {
 #pragma unroll
                     for (int t = 0; t < 8; ++t) {
                         uint2 y;
-                        y.x = (uint32_t)float_to_half_bits_rne((O[t][0] - z) * inv) |
-                              ((uint32_t)float_to_half_bits_rne((O[t][1] - z) * inv) << 16);
-                        y.y = (uint32_t)float_to_half_bits_rne((O[t][2] - z) * inv) |
-                              ((uint32_t)float_to_half_bits_rne((O[t][3] - z) * inv) << 16);
+                        y.x = (uint32_t)float_to_half_bits_rne(O[t][0] * inv) |
+                              ((uint32_t)float_to_half_bits_rne(O[t][1] * inv) << 16);
+                        y.y = (uint32_t)float_to_half_bits_rne(O[t][2] * inv) |
+                              ((uint32_t)float_to_half_bits_rne(O[t][3] * inv) << 16);
                         *reinterpret_cast<uint2*>(o + 16 * t) = y;
                     }
                 }
-            } else if (m < heads_here) {
-                // Partial 0 of this worker: the row that holds f0; 1: a later one.
-                const int64_t at = ((int64_t)me * 2 + (from >= 0 ? 0 : 1)) * A.per_chunk + m;
-                if (g == 0) A.part_ml[at] = make_float2(R, l);
-#pragma unroll
-                for (int t = 0; t < 8; ++t)
-                    *reinterpret_cast<f4_t*>(A.part_o + at * kD + 16 * t + 4 * g) = O[t] - z;
+            } else if (more) {                                    // the end of a row begun before: first partial sums
+                float l;
+                settle(l);
+                keep(reinterpret_cast<float*>(lds + kWaves * kWaveLds) + wv * A.per_chunk * kPart, l);
+                note_segment(2 * wv, f);
+            } else {
+                open = true;
+                note_segment(2 * wv + 1, f);
+            }
+            if (more) {
+                uint4 raw[4];
+                load_q(nx, raw);
+                start_row(nx, raw);
             }
         }
+        if (!more) break;
         cu = nx;
         if (f + 2 < f1) {
             advance(nx);
             fetch_page(nx);
         }
     }
+    if (A.groups == 0) return;
+
+    // ---- the workgroup's partial sums, joined row by row.
+    __syncthreads();                      // no wave needs its headers and window rows any more
+    if (open) {
+        float l;
+        settle(l);
+        keep(reinterpret_cast<float*>(lds + wv * kWaveLds), l);
+    }
+    __syncthreads();
+    // Segment 2 w + k: wave w's first (k = 0) or last row.  Their rows ascend, so
+    // a row's segments are the lanes that hold its number.
+    const int mine = lane < 2 * kWaves ? seg_row[lane] : -1;
+    const int from = lane < 2 * kWaves ? seg_begin[lane] : 0, to = lane < 2 * kWaves ? seg_end[lane] : 0;
+    uint32_t left = (uint32_t)__builtin_amdgcn_ballot_w64(mine >= 0);
+    while (left != 0) {
+        const int s0 = __builtin_ctz(left);
+        const int row = __builtin_amdgcn_readlane(mine, s0);
+        const uint32_t in = (uint32_t)__builtin_amdgcn_ballot_w64(mine == row);
+        left &= ~in;
+        const int begin = __builtin_amdgcn_readlane(from, s0), end = __builtin_amdgcn_readlane(to, s0);
+        const int entry = row / rows, in_entry = row - entry * rows;
+        const int h = in_entry / A.chunks, first = (in_entry - h * A.chunks) * A.per_chunk;
+        const int n = A.group - first < A.per_chunk ? A.group - first : A.per_chunk;
+        const bool whole = begin >= run0 && end <= run1;
+        const int64_t at = ((int64_t)blockIdx.x * 2 + (begin <= run0 ? 0 : 1)) * A.per_chunk;
+        for (int i = threadIdx.x; i < n * (kD / 4); i += kThreads) {
+            const int q_head = i / (kD / 4), c = i % (kD / 4) * 4;
+            // All of the places are read at once; those of other rows do not count.
+            float f[2 * kWaves], top = -__builtin_huge_valf(), l = 0.0f;
+            f4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
+            const auto part = [&](int s) {
+                return reinterpret_cast<const float*>(lds + (s & 1 ? (s >> 1) * kWaveLds : kWaves * kWaveLds) +
+                                                      (s & 1 ? 0 : (s >> 1) * A.per_chunk * kPart * 4)) + q_head * kPart;
+            };
+#pragma unroll
+            for (int s = 0; s < 2 * kWaves; ++s) {
+                f[s] = (in >> s) & 1 ? part(s)[kD] : -__builtin_huge_valf();
+                top = __builtin_fmaxf(top, f[s]);
+            }
+#pragma unroll
+            for (int s = 0; s < 2 * kWaves; ++s) {
+                if (!((in >> s) & 1)) continue;
+                const float w = exp2_hw(f[s] - top);
+                l = __builtin_fmaf(w, part(s)[kD + 1], l);
+                o += *reinterpret_cast<const f4_t*>(part(s) + c) * w;
+            }
+            if (whole) {
+                const float inv = 1.0f / l;
+                uint2 y;
+                y.x = (uint32_t)float_to_half_bits_rne(o[0] * inv) | ((uint32_t)float_to_half_bits_rne(o[1] * inv) << 16);
+                y.y = (uint32_t)float_to_half_bits_rne(o[2] * inv) | ((uint32_t)float_to_half_bits_rne(o[3] * inv) << 16);
+                *reinterpret_cast<uint2*>(A.out + entry * A.out_stride + (int64_t)(h * A.group + first + q_head) * kD + c) = y;
+            } else {
+                *reinterpret_cast<f4_t*>(A.part_o + (at + q_head) * kD + c) = o;
+                if (c == 0) A.part_ml[at + q_head] = make_float2(top, l);
+            }
+        }
+    }
 }
 
 // One workgroup per (row of the line, query head of the row): the partial sums
-// of the workers whose runs share the row, in their order,
+// of the workgroups whose runs share the row, in their order,
 //     out = sum_p 2^(R_p - R) O_p / sum_p 2^(R_p - R) L_p,
 // and zeros for a row without units.
-__global__ __launch_bounds__(kThreads) void paged_join_kernel(const AttnArgs A) {
-    __shared__ float acc[kWaves][kD];
+__global__ __launch_bounds__(kJoin) void paged_join_kernel(const AttnArgs A) {
+    __shared__ float acc[kJoin / 64][kD];
     const int rows = (int)A.c.heads * A.chunks;
     const int entry = blockIdx.x / rows, row = blockIdx.x - entry * rows;
     const int h = row / A.chunks, first = (row - h * A.chunks) * A.per_chunk, n = blockIdx.y;
@@ -595,12 +861,11 @@ __global__ __launch_bounds__(kThreads) void paged_join_kernel(const AttnArgs A) 
         if (threadIdx.x < kD / 2) reinterpret_cast<uint32_t*>(out)[threadIdx.x] = 0;
         return;
     }
-    // Worker of unit f: the last w with w * total / W <= f.
-    const int W = A.workers < total ? A.workers : total;
-    const int64_t a = begin + (int64_t)row * units, b = a + units;
-    const int w0 = (int)(((a + 1) * W - 1) / total), w1 = (int)((b * W - 1) / total);
-    if (w0 == w1) return;                                    // written by its wave
-    const int head0 = (int64_t)w0 * total / W == a ? 0 : 1;  // where the first worker's part is
+    const Share share(total, A.groups < total ? A.groups : total);
+    const int a = begin + row * units;
+    const int w0 = share.of(a), w1 = share.of(a + units - 1);
+    if (w0 == w1) return;                            // written by its workgroup
+    const int head0 = share.begin(w0) == a ? 0 : 1;  // where the first one's part is
     const auto part = [&](int w) { return ((int64_t)w * 2 + (w == w0 ? head0 : 0)) * A.per_chunk + n; };
     float R = -__builtin_huge_valf();
     for (int w = w0 + lane; w <= w1; w += 64) R = __builtin_fmaxf(R, A.part_ml[part(w)].x);
@@ -614,7 +879,7 @@ __global__ __launch_bounds__(kThreads) void paged_join_kernel(const AttnArgs A) 
     l = group_sum<64>(l);
     float2 o = make_float2(0.0f, 0.0f);
 #pragma unroll 4
-    for (int w = w0 + wv; w <= w1; w += kWaves) {
+    for (int w = w0 + wv; w <= w1; w += kJoin / 64) {
         const int64_t at = part(w);
         const float f = exp2_hw(A.part_ml[at].x - R);
         const float2 v = *reinterpret_cast<const float2*>(A.part_o + at * kD + 2 * lane);
@@ -627,7 +892,7 @@ __global__ __launch_bounds__(kThreads) void paged_join_kernel(const AttnArgs A) 
     if (threadIdx.x < kD) {
         float v = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kWaves; ++k) v += acc[k][threadIdx.x];
+        for (int k = 0; k < kJoin / 64; ++k) v += acc[k][threadIdx.x];
         out[threadIdx.x] = float_to_half_bits_rne(v / l);
     }
 }
@@ -653,26 +918,28 @@ hipError_t launch_paged_attention(const void* q, int64_t q_stride, int64_t q_hea
     A.per_chunk = (A.group + A.chunks - 1) / A.chunks;
     A.chunks = (A.group + A.per_chunk - 1) / A.per_chunk;
     A.scale = scale * 1.4426950408889634f;
-    // Two waves per SIMD (the registers of a wave leave room for two), but no
-    // more than there can be units.
+    // One workgroup of eight waves per compute unit (two waves fill a SIMD's
+    // registers), but no more than there can be units.
     const int64_t rows = count * c.heads * A.chunks, most = rows * (c.max_pages + 4);
-    const int64_t workers = 8 * (int64_t)num_cus < most ? 8 * (int64_t)num_cus : most;
+    const int64_t groups = num_cus < most ? num_cus : most;
     const size_t prefix_bytes = ((size_t)(count + 1) * 4 + 15) / 16 * 16;
-    const size_t parts = (size_t)workers * 2 * A.per_chunk;
+    const size_t parts = (size_t)groups * 2 * A.per_chunk;
     if (ws.sizing()) {
         ws.want(prefix_bytes + (parts * sizeof(float2) + 15) / 16 * 16 + parts * kD * sizeof(float));
         return hipSuccess;
     }
     uint8_t* at = static_cast<uint8_t*>(ws.ptr);
-    A.workers = at ? (int)workers : 0;
+    A.groups = at ? (int)groups : 0;
     A.prefix = reinterpret_cast<int32_t*>(at);
     A.part_ml = reinterpret_cast<float2*>(at + prefix_bytes);
     A.part_o = reinterpret_cast<float*>(at + prefix_bytes + (parts * sizeof(float2) + 15) / 16 * 16);
-    const int64_t waves = at ? workers : rows;
-    paged_attn_kernel<<<dim3((unsigned)((waves + kWaves - 1) / kWaves)), dim3(kThreads), 0, stream>>>(A);
+    const int64_t grid = at ? groups : (rows + kWaves - 1) / kWaves;
+    const size_t lds = kWaves * (kWaveLds + (size_t)A.per_chunk * kPart * sizeof(float));
+    const auto kernel = A.per_chunk <= 4 ? paged_attn_kernel<1> : A.per_chunk <= 8 ? paged_attn_kernel<2> : paged_attn_kernel<4>;
+    kernel<<<dim3((unsigned)grid), dim3(kThreads), lds, stream>>>(A);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !at) return e;
-    paged_join_kernel<<<dim3((unsigned)rows, (unsigned)A.per_chunk), dim3(kThreads), 0, stream>>>(A);
+    paged_join_kernel<<<dim3((unsigned)rows, (unsigned)A.per_chunk), dim3(kJoin), 0, stream>>>(A);
     return hipGetLastError();
 }
 
