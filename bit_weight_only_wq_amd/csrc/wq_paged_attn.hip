@@ -794,22 +794,40 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
     }
     __syncthreads();
     // Segment 2 w + k: wave w's first (k = 0) or last row.  Their rows ascend, so
-    // a row's segments are the lanes that hold its number.
+    // a row's segments are the lanes that hold its number.  Lane k takes the
+    // k-th row's description; then the waves share the rows' (head, channel)
+    // places, 64 at a time.
     const int mine = lane < 2 * kWaves ? seg_row[lane] : -1;
     const int from = lane < 2 * kWaves ? seg_begin[lane] : 0, to = lane < 2 * kWaves ? seg_end[lane] : 0;
     uint32_t left = (uint32_t)__builtin_amdgcn_ballot_w64(mine >= 0);
-    while (left != 0) {
+    int joins = 0, k_row = 0, k_begin = 0, k_end = 0;
+    uint32_t k_in = 0;
+    for (; left != 0; ++joins) {
         const int s0 = __builtin_ctz(left);
         const int row = __builtin_amdgcn_readlane(mine, s0);
         const uint32_t in = (uint32_t)__builtin_amdgcn_ballot_w64(mine == row);
         left &= ~in;
         const int begin = __builtin_amdgcn_readlane(from, s0), end = __builtin_amdgcn_readlane(to, s0);
+        if (lane == joins) {
+            k_row = row;
+            k_begin = begin;
+            k_end = end;
+            k_in = in;
+        }
+    }
+    const int tasks = (A.per_chunk * (kD / 4) + 63) / 64;            // of a row
+    for (int task = wv; task < joins * tasks; task += kWaves) {
+        const int k = task / tasks;
+        const int row = __builtin_amdgcn_readlane(k_row, k), begin = __builtin_amdgcn_readlane(k_begin, k);
+        const int end = __builtin_amdgcn_readlane(k_end, k);
+        const uint32_t in = (uint32_t)__builtin_amdgcn_readlane((int)k_in, k);
         const int entry = row / rows, in_entry = row - entry * rows;
         const int h = in_entry / A.chunks, first = (in_entry - h * A.chunks) * A.per_chunk;
         const int n = A.group - first < A.per_chunk ? A.group - first : A.per_chunk;
         const bool whole = begin >= run0 && end <= run1;
         const int64_t at = ((int64_t)blockIdx.x * 2 + (begin <= run0 ? 0 : 1)) * A.per_chunk;
-        for (int i = threadIdx.x; i < n * (kD / 4); i += kThreads) {
+        const int i = (task - k * tasks) * 64 + lane;
+        if (i < n * (kD / 4)) {
             const int q_head = i / (kD / 4), c = i % (kD / 4) * 4;
             // All of the places are read at once; those of other rows do not count.
             float f[2 * kWaves], top = -__builtin_huge_valf(), l = 0.0f;
