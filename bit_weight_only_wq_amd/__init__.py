@@ -577,7 +577,7 @@ def kv_paged_attention(q, cache: PagedKV, lens, seqs=None, window: int = 0, scal
     tokens lens says each slot holds.  seqs as in kv_paged_append; window > 0
     keeps the last `window` tokens; scale defaults to 1 / sqrt(128).  The
     workspace comes from torch or from `workspace` (kv_paged_workspace);
-    use_workspace=False walks each sequence and KV head with one wavefront."""
+    use_workspace=False gives each sequence and KV head one workgroup."""
     import torch
     dev = cache.device
     qs = _heads_rows(q, None, "q", dev)

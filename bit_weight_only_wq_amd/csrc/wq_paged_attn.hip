@@ -68,7 +68,7 @@ constexpr int kMaxRow = 16;               // query heads of a row (columns of a 
 constexpr int kQuarter = 32;              // window tokens of a unit
 constexpr int kVHalf = kD / 2;            // channels of a window unit's V in LDS at a time
 constexpr int kVRow = kVHalf + 8;         // fp16 elements of such a row
-constexpr int kPart = kD + 4;             // floats of one head's partial sums in LDS: 128 O, R, L
+constexpr int kPart = kD + 4;             // floats of one head's partial sums in LDS: 128 O, R, L, zeros
 constexpr int kJoin = 256;                // threads of the joining kernel
 constexpr int kBufWord3 = 0x00020000;     // raw, unswizzled gfx9 buffer
 
@@ -82,7 +82,7 @@ struct AttnArgs {
     int count;
     int group;                            // query heads per KV head
     int chunks, per_chunk;                // rows per KV head, query heads of each (the last may have fewer)
-    int groups;                           // workgroups that share the line; 0: one wave per row
+    int groups;                           // workgroups that share the line; 0: one workgroup per row
     float scale;                          // times log2(e)
     int32_t* prefix;                      // [count + 1] units before each entry
     float2* part_ml;                      // [groups][2][per_chunk] R and sum
@@ -154,6 +154,10 @@ __device__ __forceinline__ uint32_t word(const uint4& u, int i) { return i == 0 
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
+__device__ __forceinline__ uint32_t half_pair(float a, float b) {
+    return as_u32(h2_t{(_Float16)a, (_Float16)b});
+}
+
 // Largest value over the four lanes of an m.
 __device__ __forceinline__ float column_max(float v) {
     v = __builtin_fmaxf(v, __shfl_xor(v, 16, 64));
@@ -222,7 +226,7 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
     const int g = lane >> 4, m = lane & 15;
     const int rows = (int)A.c.heads * A.chunks;                          // of an entry
     uint16_t* head_lds = reinterpret_cast<uint16_t*>(lds + wv * kWaveLds);
-    uint4* q_lds = reinterpret_cast<uint4*>(lds + wv * kWaveLds + 1024) + lane;   // + 64 j
+    const auto q_lds = [&](int j) { return reinterpret_cast<uint4*>(lds + wv * kWaveLds + 1024) + anew(lane) + 64 * j; };
     uint16_t* p_lds = head_lds + (1024 + 4096) / 2;
     uint16_t* v_lds = p_lds + 16 * kPWindow;
     const bool m_lo = kSplit && (m & 1);  // slot m holds lo halves
@@ -234,21 +238,20 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
     int f0, f1;
     cu.unit = 0;
     int run0 = 0, run1 = 0;               // the workgroup's run
-    if (A.groups == 0) {                  // one wave per row
-        const int me = (int)blockIdx.x * kWaves + wv;
-        if (me >= A.count * rows) return;
-        cu.entry = me / rows;
-        cu.row = me - cu.entry * rows;
+    if (A.groups == 0) {                  // one workgroup per row
+        cu.entry = (int)blockIdx.x / rows;
+        cu.row = (int)blockIdx.x - cu.entry * rows;
         ch.load(A, cu.entry & ~63, lane);
-        f0 = 0;
-        f1 = span_of(__builtin_amdgcn_readlane(ch.len, cu.entry & 63), A.window).units();
-        if (f1 == 0) {                    // nothing to see: zeros
+        run1 = span_of(__builtin_amdgcn_readlane(ch.len, cu.entry & 63), A.window).units();
+        if (run1 == 0) {                  // nothing to see: zeros
             const int h = cu.row / A.chunks, first = (cu.row - h * A.chunks) * A.per_chunk;
             const int n = A.group - first < A.per_chunk ? A.group - first : A.per_chunk;
             uint32_t* o = reinterpret_cast<uint32_t*>(A.out + cu.entry * A.out_stride + (int64_t)(h * A.group + first) * kD);
-            for (int i = lane; i < n * (kD / 2); i += 64) o[i] = 0;
+            for (int i = threadIdx.x; i < n * (kD / 2); i += kThreads) o[i] = 0;
             return;
         }
+        f0 = cu.unit = run1 * wv / kWaves;
+        f1 = run1 * (wv + 1) / kWaves;
     } else {
         int total = 0, u = 0, inc = 0;
         const auto scan = [&](int at) {   // units of 64 entries, and their running sum
@@ -278,7 +281,7 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
         const int find = f0 < f1 ? f0 : run0;            // (a wave without units looks at any)
         int before = 0;
         for (int at = 0;; at += 64) {     // ends: find < total
-            if (A.count > 64) scan(at);
+            if (A.count > 64) scan(at);   // (else it is still there)
             const uint64_t past = __builtin_amdgcn_ballot_w64(before + inc > find);
             if (past != 0) {
                 const int i = __builtin_ctzll(past);
@@ -352,23 +355,21 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
 
     const float zero = __builtin_bit_cast(float, vgpr_const(0));
 
-    // A row's queries as they lie: 32 channels of this lane's head.
-    const auto load_q = [&](const Cursor& c, uint4 (&raw)[4]) {
+    // A row's queries as they lie, 4 NH heads of 256 bytes: 16-byte piece lane +
+    // 64 k of them.
+    const auto load_q = [&](const Cursor& c, uint4 (&piece)[NH]) {
         const int n = A.group - c.first < A.per_chunk ? A.group - c.first : A.per_chunk;
-        const int mq = anew(m), gq = anew(g);
+        const int lq = anew(lane);
+        const uint4* src = reinterpret_cast<const uint4*>(A.q + c.entry * A.q_stride + (int64_t)(c.head * A.group + c.first) * kD);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) raw[j] = make_uint4(0, 0, 0, 0);
-        const int hq = (mq >> 2) + 4 * (kSplit ? (mq & 3) >> 1 : mq & 3);
-        if (hq < n && (NH > 1 || (mq & 3) < 2)) {
-            const uint4* src = reinterpret_cast<const uint4*>(A.q + c.entry * A.q_stride +
-                                                              (int64_t)(c.head * A.group + c.first + hq) * kD + 32 * gq);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) raw[j] = src[j];
+        for (int k = 0; k < NH; ++k) {
+            piece[k] = make_uint4(0, 0, 0, 0);
+            if ((lq >> 4) + 4 * k < n) piece[k] = src[lq + 64 * k];
         }
     };
 
-    uint4 K[8], V[8], H, raw0[4];
-    load_q(cu, raw0);
+    uint4 K[8], V[8], H, piece0[NH];
+    load_q(cu, piece0);
     fetch_page(cu);
     {
         const auto r = buffer(cu, f0 < f1);
@@ -389,8 +390,13 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
     bool bad = false, in_blocks = false;
     int heads_here = 0;                   // query heads of the row
 
-    // A new row, from its queries: |q| < 2 by a power of two that cn undoes.
-    const auto start_row = [&](const Cursor& c, const uint4 (&raw)[4]) {
+    const auto turned = [&]() {               // the wave's LDS writes before its reads that follow
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    };
+    // A new row, from its queries: turned through LDS to the slots' lanes, |q| < 2
+    // by a power of two that cn undoes.
+    const auto start_row = [&](const Cursor& c, const uint4 (&piece)[NH]) {
         bad = false;
         in_blocks = true;
         heads_here = A.group - c.first < A.per_chunk ? A.group - c.first : A.per_chunk;
@@ -401,36 +407,42 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) O[i] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
-        float top = 0.0f;
+        uint4* q_raw = reinterpret_cast<uint4*>(p_lds);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int k = 0; k < NH; ++k) q_raw[anew(lane) + 64 * k] = piece[k];
+        turned();
+        const int mq = anew(m), hq = (mq >> 2) + 4 * (kSplit ? (mq & 3) >> 1 : mq & 3);
+        const bool none = NH == 1 && (mq & 3) >= 2;
+        uint4 raw[4];
+        us2_t top2 = us2_t{0, 0};             // (magnitudes order as their bits do)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const h2_t v = as_h2(word(raw[j], i));
-                top = __builtin_fmaxf(top, __builtin_fmaxf(__builtin_fabsf((float)v.x), __builtin_fabsf((float)v.y)));
-            }
-        top = column_max(top);
+        for (int j = 0; j < 4; ++j) {
+            raw[j] = none ? make_uint4(0, 0, 0, 0) : q_raw[16 * (none ? 0 : hq) + 4 * anew(g) + j];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                top2 = __builtin_elementwise_max(top2, __builtin_bit_cast(us2_t, word(raw[j], i) & 0x7FFF7FFFu));
+        }
+        turned();                             // (read before the weights come to the same place)
+        const float top = column_max(half_bits_to_float(top2.x > top2.y ? top2.x : top2.y));
         const int e = top > 0.0f ? __builtin_amdgcn_frexp_expf(top) - 1 : 0;   // top * 2^-e in [1, 2)
         // (Within 2^-120 .. 2^80: no product with an infinity is 0 * inf.)
         const float unit = __builtin_amdgcn_fmed3f(__builtin_amdgcn_ldexpf(__builtin_fabsf(A.scale), e), 0x1p-120f, 0x1p80f);
 #pragma unroll
-        for (int u = 0; u < NH; ++u) cn[u] = __shfl(unit, 4 * g + (kSplit ? 2 * u : u), 64);   // from the head's slot
-        const float sign = A.scale < 0.0f ? -1.0f : 1.0f;
+        for (int u = 0; u < NH; ++u) cn[u] = __shfl(unit, 4 * anew(g) + (kSplit ? 2 * u : u), 64);   // from the head's slot
+        // 2^-e in two factors that fp16 holds, the second with scale's sign.
+        const int e1 = -e / 2, e2 = -e - e1;
+        const _Float16 f1_ = (_Float16)__builtin_amdgcn_ldexpf(1.0f, e1);
+        const _Float16 f2_ = (_Float16)__builtin_amdgcn_ldexpf(A.scale < 0.0f ? -1.0f : 1.0f, e2);
+        const uint32_t f1 = as_u32(h2_t{f1_, f1_}), f2 = as_u32(h2_t{f2_, f2_}), f2s = pk_mul(f2, kSixteenth);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const h2_t v = as_h2(word(raw[j], i));
-                w[i] = as_u32(h2_t{(_Float16)__builtin_amdgcn_ldexpf(sign * (float)v.x, -e),
-                                   (_Float16)__builtin_amdgcn_ldexpf(sign * (float)v.y, -e)});
-            }
             // To LDS (16 registers), in code order, the odd channels / 16.
-            const uint4 c4 = code_order(make_uint4(w[0], w[1], w[2], w[3]));
-            q_lds[64 * j] = make_uint4(c4.x, pk_mul(c4.y, kSixteenth), c4.z, pk_mul(c4.w, kSixteenth));
+            const uint4 c4 = code_order(raw[j]);
+            *q_lds(j) = make_uint4(pk_mul(pk_mul(c4.x, f1), f2), pk_mul(pk_mul(c4.y, f1), f2s),
+                                       pk_mul(pk_mul(c4.z, f1), f2), pk_mul(pk_mul(c4.w, f1), f2s));
         }
     };
-    start_row(cu, raw0);
+    start_row(cu, piece0);
 
     // What the lanes of head g + 4 u hold, for the lanes of a slot m of it.
     const auto to_slot = [&](const float (&v)[NH]) {
@@ -443,36 +455,27 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
         }
         return r;
     };
-    // A row's sums as they are (in both of a head's slots): all tokens together,
-    // the zero points taken out.
-    const auto settle = [&](float& l) {
-        float ls[NH], zs[NH];
-#pragma unroll
-        for (int u = 0; u < NH; ++u) {
-            ls[u] = group_sum<16>(L[u]);
-            zs[u] = group_sum<16>(cz[u]);
-        }
-        const float z = to_slot(zs);
-        l = bad ? __builtin_nanf("") : to_slot(ls);
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            if (in_blocks) O[t] *= kVUnit;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) O[t][i] = (kSplit ? O[t][i] + dpp_f<0xB1>(O[t][i]) : O[t][i]) - z;
-        }
-    };
     // The head (of the row) that this lane writes sums of, or -1.
     const auto my_head = [&]() {
         const int mt = anew(m), h = (mt >> 2) + 4 * (kSplit ? (mt & 3) >> 1 : mt & 3);
         return h < heads_here && !(kSplit && (mt & 1)) && (NH > 1 || (mt & 3) < 2) ? h : -1;
     };
-    const auto keep = [&](float* part, float l) {   // partial sums to LDS
-        const float r = to_slot(R);
+    // A slot's two halves together (in both slots).
+    const auto both = [&](float v) { return kSplit ? v + dpp_f<0xB1>(v) : v; };
+    const auto total_l = [&](int u) { return bad ? __builtin_nanf("") : group_sum<16>(L[u]); };
+    const auto keep = [&](float* part) {      // partial sums to LDS
+        const float k = in_blocks ? kVUnit : 1.0f;
         const int h = my_head(), gp = anew(g);
-        if (h < 0) return;
 #pragma unroll
-        for (int t = 0; t < 8; ++t) *reinterpret_cast<f4_t*>(part + h * kPart + 16 * t + 4 * gp) = O[t];
-        if (gp == 0) *reinterpret_cast<float2*>(part + h * kPart + kD) = make_float2(r, l);
+        for (int t = 0; t < 8; ++t) {
+            const f4_t o = {both(O[t][0]) * k, both(O[t][1]) * k, both(O[t][2]) * k, both(O[t][3]) * k};
+            if (h >= 0) *reinterpret_cast<f4_t*>(part + h * kPart + 16 * t + 4 * gp) = o;
+        }
+#pragma unroll
+        for (int u = 0; u < NH; ++u) {
+            const f4_t s = {R[u], total_l(u), group_sum<16>(cz[u]), 0.0f};
+            if (anew(m) == 0 && gp + 4 * u < heads_here) *reinterpret_cast<f4_t*>(part + (gp + 4 * u) * kPart + kD) = s;
+        }
     };
     const auto note_segment = [&](int at, int f) {
         if (lane == 0) {
@@ -485,6 +488,10 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
 
     for (int f = f0; f < f1; ++f) {
         const bool more = f + 1 < f1;
+        // The next row's queries, ahead of the next unit's codes (past 8 heads
+        // there are no registers for them: they are loaded where it starts).
+        uint4 piece[NH];
+        if (kSplit && more && nx.unit == 0) load_q(nx, piece);
         const auto nbuf = buffer(nx, more);
 
         // New reference for the running exponent, and what is held with the old one.
@@ -516,15 +523,10 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
             hi = as_u32(h);
             lo = as_u32(h2_t{(_Float16)(w0 - (float)h.x), (_Float16)(w1 - (float)h.y)});
         };
-        const auto turned = [&]() {           // the wave's LDS writes before its reads that follow
-            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-        };
-
         if (cu.block()) {
             bad |= cu.page < 0 || cu.page >= A.c.num_pages;
             // Headers to LDS: 16 bytes a lane in, the lane's 64 bytes of each out.
-            *reinterpret_cast<uint4*>(head_lds + 8 * lane) = H;
+            *reinterpret_cast<uint4*>(head_lds + 8 * anew(lane)) = H;
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
             __builtin_amdgcn_wave_barrier();
             const uint4* hd = reinterpret_cast<const uint4*>(head_lds) + 4 * g;   // + 16 per header array
@@ -532,7 +534,7 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
             f4_t z4 = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const uint4 s = code_order(hd[j]), qj = q_lds[64 * j];
+                const uint4 s = code_order(hd[j]), qj = *q_lds(j);
                 uint4 z = code_order(hd[16 + j]);       // in the codes' units (exact: at most 11 bits, above 2^-24)
                 z = make_uint4(pk_mul(z.x, kEvenUnit), pk_mul(z.y, kOddUnit), pk_mul(z.z, kEvenUnit), pk_mul(z.w, kOddUnit));
                 a0[j] = make_uint4(pk_mul(qj.x, s.x), pk_mul(qj.y, s.y), pk_mul(qj.z, s.z), pk_mul(qj.w, s.w));
@@ -661,7 +663,7 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
             f4_t S[2] = {};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const uint4 c4 = q_lds[64 * j];    // (exact: the lo slots hold nothing)
+                const uint4 c4 = *q_lds(j);    // (exact: the lo slots hold nothing)
                 const uint4 qw = m_lo ? make_uint4(0, 0, 0, 0)
                                       : make_uint4(c4.x, pk_mul(c4.y, kSixteen), c4.z, pk_mul(c4.w, kSixteen));
 #pragma unroll
@@ -745,36 +747,31 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
         // ---- the end of the row, or of this wave's part of it.
         if (!more || cu.unit + 1 == cu.units) {
             if (cu.unit <= f - f0 && cu.unit + 1 == cu.units) {   // all of the row was here
-                float l;
-                settle(l);
-                const float inv = 1.0f / l;
+                float inv_u[NH], z_u[NH];
+#pragma unroll
+                for (int u = 0; u < NH; ++u) {
+                    inv_u[u] = 1.0f / total_l(u);
+                    z_u[u] = group_sum<16>(cz[u]) * inv_u[u];
+                }
+                const float inv = to_slot(inv_u), z = to_slot(z_u), k = in_blocks ? inv * kVUnit : inv;
                 const int mo = my_head();
                 uint16_t* o = A.out + cu.entry * A.out_stride + (int64_t)(cu.head * A.group + cu.first + mo) * kD + 4 * anew(g);
-                if (mo >= 0) {
 #pragma unroll
-                    for (int t = 0; t < 8; ++t) {
-                        uint2 y;
-                        y.x = (uint32_t)float_to_half_bits_rne(O[t][0] * inv) |
-                              ((uint32_t)float_to_half_bits_rne(O[t][1] * inv) << 16);
-                        y.y = (uint32_t)float_to_half_bits_rne(O[t][2] * inv) |
-                              ((uint32_t)float_to_half_bits_rne(O[t][3] * inv) << 16);
-                        *reinterpret_cast<uint2*>(o + 16 * t) = y;
-                    }
+                for (int t = 0; t < 8; ++t) {
+                    float v[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf(both(O[t][i]), k, -z);
+                    if (mo >= 0) *reinterpret_cast<uint2*>(o + 16 * t) = make_uint2(half_pair(v[0], v[1]), half_pair(v[2], v[3]));
                 }
             } else if (more) {                                    // the end of a row begun before: first partial sums
-                float l;
-                settle(l);
-                keep(reinterpret_cast<float*>(lds + kWaves * kWaveLds) + wv * A.per_chunk * kPart, l);
+                keep(reinterpret_cast<float*>(lds + kWaves * kWaveLds) + wv * A.per_chunk * kPart);
                 note_segment(2 * wv, f);
             } else {
                 open = true;
                 note_segment(2 * wv + 1, f);
             }
-            if (more) {
-                uint4 raw[4];
-                load_q(nx, raw);
-                start_row(nx, raw);
-            }
+            if (!kSplit && more) load_q(nx, piece);
+            if (more) start_row(nx, piece);
         }
         if (!more) break;
         cu = nx;
@@ -783,15 +780,9 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
             fetch_page(nx);
         }
     }
-    if (A.groups == 0) return;
-
     // ---- the workgroup's partial sums, joined row by row.
     __syncthreads();                      // no wave needs its headers and window rows any more
-    if (open) {
-        float l;
-        settle(l);
-        keep(reinterpret_cast<float*>(lds + wv * kWaveLds), l);
-    }
+    if (open) keep(reinterpret_cast<float*>(lds + wv * kWaveLds));
     __syncthreads();
     // Segment 2 w + k: wave w's first (k = 0) or last row.  Their rows ascend, so
     // a row's segments are the lanes that hold its number.  Lane k takes the
@@ -829,33 +820,36 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
         const int i = (task - k * tasks) * 64 + lane;
         if (i < n * (kD / 4)) {
             const int q_head = i / (kD / 4), c = i % (kD / 4) * 4;
-            // All of the places are read at once; those of other rows do not count.
-            float f[2 * kWaves], top = -__builtin_huge_valf(), l = 0.0f;
-            f4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
-            const auto part = [&](int s) {
-                return reinterpret_cast<const float*>(lds + (s & 1 ? (s >> 1) * kWaveLds : kWaves * kWaveLds) +
-                                                      (s & 1 ? 0 : (s >> 1) * A.per_chunk * kPart * 4)) + q_head * kPart;
-            };
+            // A wave has one segment of the row at most.  All are read at once; what
+            // lies in the places of the others (anything) does not count.
+            f4_t o[kWaves], st[kWaves];
+            float top = -__builtin_huge_valf(), l = 0.0f;
 #pragma unroll
-            for (int s = 0; s < 2 * kWaves; ++s) {
-                f[s] = (in >> s) & 1 ? part(s)[kD] : -__builtin_huge_valf();
-                top = __builtin_fmaxf(top, f[s]);
+            for (int w = 0; w < kWaves; ++w) {
+                const bool is_first = (in >> (2 * w)) & 1, has = (in >> (2 * w)) & 3;
+                const float* part = reinterpret_cast<const float*>(lds + (is_first ? kWaves * kWaveLds + w * A.per_chunk * kPart * 4
+                                                                                   : w * kWaveLds)) + q_head * kPart;
+                st[w] = *reinterpret_cast<const f4_t*>(part + kD);
+                o[w] = *reinterpret_cast<const f4_t*>(part + c);
+                if (!has) {
+                    st[w] = f4_t{-__builtin_huge_valf(), 0.0f, 0.0f, 0.0f};
+                    o[w] = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
+                }
+                top = __builtin_fmaxf(top, st[w][0]);
             }
+            f4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int s = 0; s < 2 * kWaves; ++s) {
-                if (!((in >> s) & 1)) continue;
-                const float w = exp2_hw(f[s] - top);
-                l = __builtin_fmaf(w, part(s)[kD + 1], l);
-                o += *reinterpret_cast<const f4_t*>(part(s) + c) * w;
+            for (int w = 0; w < kWaves; ++w) {
+                const float f = exp2_hw(st[w][0] - top);
+                l = __builtin_fmaf(f, st[w][1], l);
+                sum += (o[w] - st[w][2]) * f;
             }
             if (whole) {
                 const float inv = 1.0f / l;
-                uint2 y;
-                y.x = (uint32_t)float_to_half_bits_rne(o[0] * inv) | ((uint32_t)float_to_half_bits_rne(o[1] * inv) << 16);
-                y.y = (uint32_t)float_to_half_bits_rne(o[2] * inv) | ((uint32_t)float_to_half_bits_rne(o[3] * inv) << 16);
-                *reinterpret_cast<uint2*>(A.out + entry * A.out_stride + (int64_t)(h * A.group + first + q_head) * kD + c) = y;
+                *reinterpret_cast<uint2*>(A.out + entry * A.out_stride + (int64_t)(h * A.group + first + q_head) * kD + c) =
+                    make_uint2(half_pair(sum[0] * inv, sum[1] * inv), half_pair(sum[2] * inv, sum[3] * inv));
             } else {
-                *reinterpret_cast<f4_t*>(A.part_o + (at + q_head) * kD + c) = o;
+                *reinterpret_cast<f4_t*>(A.part_o + (at + q_head) * kD + c) = sum;
                 if (c == 0) A.part_ml[at + q_head] = make_float2(top, l);
             }
         }
@@ -940,18 +934,24 @@ hipError_t launch_paged_attention(const void* q, int64_t q_stride, int64_t q_hea
     // registers), but no more than there can be units.
     const int64_t rows = count * c.heads * A.chunks, most = rows * (c.max_pages + 4);
     const int64_t groups = num_cus < most ? num_cus : most;
+    // A few rows of at most 16 units: one workgroup each, two units a wave, and
+    // no second kernel (32 rows of 7 units 12.0 us instead of 14.2; with more
+    // rows than compute units the equal runs win, 4096 rows of 2 units 80 us
+    // instead of 152).
+    const bool short_rows = c.max_pages + 4 <= 16 && rows <= num_cus;
     const size_t prefix_bytes = ((size_t)(count + 1) * 4 + 15) / 16 * 16;
     const size_t parts = (size_t)groups * 2 * A.per_chunk;
     if (ws.sizing()) {
+        if (short_rows) return hipSuccess;
         ws.want(prefix_bytes + (parts * sizeof(float2) + 15) / 16 * 16 + parts * kD * sizeof(float));
         return hipSuccess;
     }
-    uint8_t* at = static_cast<uint8_t*>(ws.ptr);
+    uint8_t* at = short_rows ? nullptr : static_cast<uint8_t*>(ws.ptr);
     A.groups = at ? (int)groups : 0;
     A.prefix = reinterpret_cast<int32_t*>(at);
     A.part_ml = reinterpret_cast<float2*>(at + prefix_bytes);
     A.part_o = reinterpret_cast<float*>(at + prefix_bytes + (parts * sizeof(float2) + 15) / 16 * 16);
-    const int64_t grid = at ? groups : (rows + kWaves - 1) / kWaves;
+    const int64_t grid = at ? groups : rows;
     const size_t lds = kWaves * (kWaveLds + (size_t)A.per_chunk * kPart * sizeof(float));
     const auto kernel = A.per_chunk <= 4 ? paged_attn_kernel<1> : A.per_chunk <= 8 ? paged_attn_kernel<2> : paged_attn_kernel<4>;
     kernel<<<dim3((unsigned)grid), dim3(kThreads), lds, stream>>>(A);

@@ -515,7 +515,8 @@ wq_status wq_kv_paged_append(const void* k, const void* v, int64_t tokens, int64
  * atomics), but on the batch: the work of all entries is cut into equal parts,
  * and where a part ends inside a sequence, its sums are joined by a second
  * kernel through the workspace (wq_kv_paged_workspace_size).  Without a
- * workspace one wavefront walks each sequence and KV head.
+ * workspace, or for a few short sequences, one workgroup takes each sequence
+ * and KV head (and each 16 of its query heads).
  * count <= 65535, count * q_heads < 2^24 and count * q_heads * (max_pages + 4)
  * < 2^31 (WQ_ERR_UNSUPPORTED otherwise).
  */
