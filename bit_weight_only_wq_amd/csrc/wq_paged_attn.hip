@@ -69,6 +69,7 @@ constexpr int kQuarter = 32;              // window tokens of a unit
 constexpr int kVHalf = kD / 2;            // channels of a window unit's V in LDS at a time
 constexpr int kVRow = kVHalf + 8;         // fp16 elements of such a row
 constexpr int kPart = kD + 4;             // floats of one head's partial sums in LDS: 128 O, R, L, zeros
+constexpr int kMaxCount = 65536;          // entries of a call (the C entry point takes fewer)
 constexpr int kJoin = 256;                // threads of the joining kernel
 constexpr int kBufWord3 = 0x00020000;     // raw, unswizzled gfx9 buffer
 
@@ -84,7 +85,8 @@ struct AttnArgs {
     int chunks, per_chunk;                // rows per KV head, query heads of each (the last may have fewer)
     int groups;                           // workgroups that share the line; 0: one workgroup per row
     float scale;                          // times log2(e)
-    int32_t* prefix;                      // [count + 1] units before each entry
+    int4* cross;                          // [groups] the row that begins in a run and goes past it: row (or -1),
+                                          // end of its units, which partial; [groups].w is the number of units
     float2* part_ml;                      // [groups][2][per_chunk] R and sum
     float* part_o;                        // [groups][2][per_chunk][128]
 };
@@ -221,6 +223,7 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
     constexpr bool kSplit = NH <= 2;      // hi and lo in slots of their own
     // [kWaves][kWaveLds], then [kWaves][per_chunk][kPart] first partial sums.
     extern __shared__ __align__(16) uint8_t lds[];
+    __shared__ int chunk_units[kMaxCount / 64];
     __shared__ int seg_row[2 * kWaves], seg_begin[2 * kWaves], seg_end[2 * kWaves];   // (2 wave + 0 first, 1 last)
     const int lane = threadIdx.x & 63, wv = uniform(threadIdx.x >> 6);
     const int g = lane >> 4, m = lane & 15;
@@ -263,15 +266,29 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
                 if (lane >= o) inc += up;
             }
         };
-        const bool note = blockIdx.x == 0 && wv == 0;
-        for (int at = 0; at < A.count; at += 64) {
-            scan(at);
-            if (note && at + lane < A.count) A.prefix[at + lane] = total + inc - u;
-            total += __builtin_amdgcn_readlane(inc, 63);
+        // More than 64 entries: the waves share them, and each takes the sums of
+        // 64 from LDS.
+        const int chunks = (A.count + 63) / 64;
+        if (chunks == 1) {
+            scan(0);
+            total = __builtin_amdgcn_readlane(inc, 63);
+        } else {
+            for (int c = wv; c < chunks; c += kWaves) {
+                scan(64 * c);
+                if (lane == 63) chunk_units[c] = inc;
+            }
+            __syncthreads();
+            for (int c = lane; c < chunks; c += 64) total += chunk_units[c];
+#pragma unroll
+            for (int o = 32; o >= 1; o >>= 1) total += __shfl_xor(total, o, 64);
+            total = uniform(total);
         }
-        if (note && lane == 0) A.prefix[A.count] = total;
         const int used = A.groups < total ? A.groups : total;
-        if ((int)blockIdx.x >= used) return;
+        if (blockIdx.x == 0 && threadIdx.x == 0) A.cross[A.groups] = make_int4(0, 0, 0, total);
+        if ((int)blockIdx.x >= used) {
+            if (threadIdx.x == 0) A.cross[blockIdx.x] = make_int4(-1, 0, 0, 0);
+            return;
+        }
         const Share share(total, used);
         run0 = share.begin(blockIdx.x);
         run1 = share.begin(blockIdx.x + 1);
@@ -279,18 +296,29 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
         f0 = run0 + (int)((int64_t)n * wv / kWaves);
         f1 = run0 + (int)((int64_t)n * (wv + 1) / kWaves);
         const int find = f0 < f1 ? f0 : run0;            // (a wave without units looks at any)
-        int before = 0;
-        for (int at = 0;; at += 64) {     // ends: find < total
-            if (A.count > 64) scan(at);   // (else it is still there)
-            const uint64_t past = __builtin_amdgcn_ballot_w64(before + inc > find);
-            if (past != 0) {
-                const int i = __builtin_ctzll(past);
-                before += __builtin_amdgcn_readlane(inc - u, i);
-                cu.entry = at + i;
-                break;
+        int before = 0, at = 0;
+        if (chunks > 1) {
+            for (int c0 = 0;; c0 += 64) {                // ends: find < total
+                int sum = c0 + lane < chunks ? chunk_units[c0 + lane] : 0, upto = sum;
+#pragma unroll
+                for (int o = 1; o < 64; o <<= 1) {
+                    const int up = __shfl_up(upto, o, 64);
+                    if (lane >= o) upto += up;
+                }
+                const uint64_t past = __builtin_amdgcn_ballot_w64(before + upto > find);
+                if (past != 0) {
+                    const int i = __builtin_ctzll(past);
+                    before += __builtin_amdgcn_readlane(upto - sum, i);
+                    at = 64 * (c0 + i);
+                    break;
+                }
+                before += __builtin_amdgcn_readlane(upto, 63);
             }
-            before += __builtin_amdgcn_readlane(inc, 63);
+            scan(at);
         }
+        const int i = __builtin_ctzll(__builtin_amdgcn_ballot_w64(before + inc > find));
+        before += __builtin_amdgcn_readlane(inc - u, i);
+        cu.entry = at + i;
         cu.unit = find - before;          // in the entry, for now
     }
     cu.entry = uniform(cu.entry);
@@ -806,6 +834,12 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
             k_in = in;
         }
     }
+    if (A.groups != 0 && wv == 0) {       // the last one may go on in the next run
+        const int k = joins > 0 ? joins - 1 : 0;
+        const int begin = __builtin_amdgcn_readlane(k_begin, k), end = __builtin_amdgcn_readlane(k_end, k);
+        const int row = joins > 0 && begin >= run0 && end > run1 ? __builtin_amdgcn_readlane(k_row, k) : -1;
+        if (lane == 0) A.cross[blockIdx.x] = make_int4(row, end, begin <= run0 ? 0 : 1, 0);
+    }
     const int tasks = (A.per_chunk * (kD / 4) + 63) / 64;            // of a row
     for (int task = wv; task < joins * tasks; task += kWaves) {
         const int k = task / tasks;
@@ -856,57 +890,81 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
     }
 }
 
-// One workgroup per (row of the line, query head of the row): the partial sums
-// of the workgroups whose runs share the row, in their order,
-//     out = sum_p 2^(R_p - R) O_p / sum_p 2^(R_p - R) L_p,
-// and zeros for a row without units.
+// Workgroup (b < groups - 1, query head of the row): the row that begins in run b
+// and goes past it, from the partial sums of the runs that share it,
+//     out = sum_p 2^(R_p - R) O_p / sum_p 2^(R_p - R) L_p:
+// thread (j, c) takes channels 4 c .. of the partial sums j, j + 8, .., then the
+// eight j's are added in order.  The other workgroups, one per entry: zeros
+// where there is nothing to see.
 __global__ __launch_bounds__(kJoin) void paged_join_kernel(const AttnArgs A) {
-    __shared__ float acc[kJoin / 64][kD];
-    const int rows = (int)A.c.heads * A.chunks;
-    const int entry = blockIdx.x / rows, row = blockIdx.x - entry * rows;
-    const int h = row / A.chunks, first = (row - h * A.chunks) * A.per_chunk, n = blockIdx.y;
-    if (first + n >= A.group) return;
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-    uint16_t* out = A.out + entry * A.out_stride + (int64_t)(h * A.group + first + n) * kD;
-    const int total = A.prefix[A.count], begin = A.prefix[entry], units = (A.prefix[entry + 1] - begin) / rows;
-    if (units == 0) {
-        if (threadIdx.x < kD / 2) reinterpret_cast<uint32_t*>(out)[threadIdx.x] = 0;
+    constexpr int kWide = kJoin / (kD / 4);
+    __shared__ f4_t acc[kWide][kD / 4];
+    __shared__ float2 acc_rl[kWide];
+    const int rows = (int)A.c.heads * A.chunks, tid = threadIdx.x;
+    if ((int)blockIdx.x >= A.groups - 1) {
+        if (blockIdx.y != 0) return;
+        const int entry = (int)blockIdx.x - (A.groups - 1);
+        const int64_t slot = slot_of(A.c, A.seqs, entry);
+        if (slot >= 0 && clamped_len(A.c, A.lens, slot) > 0) return;
+        uint2* out = reinterpret_cast<uint2*>(A.out + entry * A.out_stride);
+        for (int i = tid; i < (int)A.c.heads * A.group * (kD / 4); i += kJoin) out[i] = make_uint2(0, 0);
         return;
     }
+    const int4 x = A.cross[blockIdx.x];
+    if (x.x < 0) return;
+    const int entry = x.x / rows, row = x.x - entry * rows, q_head = blockIdx.y;
+    const int h = row / A.chunks, first = (row - h * A.chunks) * A.per_chunk;
+    if (first + q_head >= A.group) return;
+    const int total = A.cross[A.groups].w;
     const Share share(total, A.groups < total ? A.groups : total);
-    const int a = begin + row * units;
-    const int w0 = share.of(a), w1 = share.of(a + units - 1);
-    if (w0 == w1) return;                            // written by its workgroup
-    const int head0 = share.begin(w0) == a ? 0 : 1;  // where the first one's part is
-    const auto part = [&](int w) { return ((int64_t)w * 2 + (w == w0 ? head0 : 0)) * A.per_chunk + n; };
-    float R = -__builtin_huge_valf();
-    for (int w = w0 + lane; w <= w1; w += 64) R = __builtin_fmaxf(R, A.part_ml[part(w)].x);
+    const int w0 = blockIdx.x, w1 = share.of(x.y - 1);
+    const int j = tid / (kD / 4), c = tid % (kD / 4);
+    float R = -__builtin_huge_valf(), l = 0.0f;
+    f4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int w = w0 + j; w <= w1; w += 4 * kWide) {      // four at a time
+        float2 ml[4];
+        f4_t v[4];
+        float top = R;
 #pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) R = __builtin_fmaxf(R, __shfl_xor(R, o, 64));
-    float l = 0.0f;
-    for (int w = w0 + lane; w <= w1; w += 64) {
-        const float2 ml = A.part_ml[part(w)];
-        l += ml.y * exp2_hw(ml.x - R);
+        for (int k = 0; k < 4; ++k) {
+            const int p = w + k * kWide <= w1 ? w + k * kWide : w1;
+            const int64_t at = ((int64_t)p * 2 + (p == w0 ? x.z : 0)) * A.per_chunk + q_head;
+            ml[k] = A.part_ml[at];
+            v[k] = *reinterpret_cast<const f4_t*>(A.part_o + at * kD + 4 * c);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (w + k * kWide > w1) ml[k] = make_float2(-__builtin_huge_valf(), 0.0f);
+            top = __builtin_fmaxf(top, ml[k].x);
+        }
+        const float f0 = exp2_hw(R - top);
+        l *= f0;
+        o *= f0;
+        R = top;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float f = exp2_hw(ml[k].x - top);
+            l = __builtin_fmaf(f, ml[k].y, l);
+            o += v[k] * f;
+        }
     }
-    l = group_sum<64>(l);
-    float2 o = make_float2(0.0f, 0.0f);
-#pragma unroll 4
-    for (int w = w0 + wv; w <= w1; w += kJoin / 64) {
-        const int64_t at = part(w);
-        const float f = exp2_hw(A.part_ml[at].x - R);
-        const float2 v = *reinterpret_cast<const float2*>(A.part_o + at * kD + 2 * lane);
-        o.x = __builtin_fmaf(f, v.x, o.x);
-        o.y = __builtin_fmaf(f, v.y, o.y);
-    }
-    acc[wv][2 * lane] = o.x;
-    acc[wv][2 * lane + 1] = o.y;
+    acc[j][c] = o;
+    if (c == 0) acc_rl[j] = make_float2(R, l);
     __syncthreads();
-    if (threadIdx.x < kD) {
-        float v = 0.0f;
+    if (j != 0) return;
+    float top = R;
+    for (int k = 1; k < kWide; ++k) top = __builtin_fmaxf(top, acc_rl[k].x);
+    f4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    float ls = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kJoin / 64; ++k) v += acc[k][threadIdx.x];
-        out[threadIdx.x] = float_to_half_bits_rne(v / l);
+    for (int k = 0; k < kWide; ++k) {
+        const float f = exp2_hw(acc_rl[k].x - top);
+        ls = __builtin_fmaf(f, acc_rl[k].y, ls);
+        sum += acc[k][c] * f;
     }
+    const float inv = 1.0f / ls;
+    uint16_t* out = A.out + entry * A.out_stride + (int64_t)(h * A.group + first + q_head) * kD + 4 * c;
+    *reinterpret_cast<uint2*>(out) = make_uint2(half_pair(sum[0] * inv, sum[1] * inv), half_pair(sum[2] * inv, sum[3] * inv));
 }
 
 }  // namespace
@@ -939,25 +997,25 @@ hipError_t launch_paged_attention(const void* q, int64_t q_stride, int64_t q_hea
     // rows than compute units the equal runs win, 4096 rows of 2 units 80 us
     // instead of 152).
     const bool short_rows = c.max_pages + 4 <= 16 && rows <= num_cus;
-    const size_t prefix_bytes = ((size_t)(count + 1) * 4 + 15) / 16 * 16;
+    const size_t cross_bytes = (size_t)(groups + 1) * sizeof(int4);
     const size_t parts = (size_t)groups * 2 * A.per_chunk;
     if (ws.sizing()) {
         if (short_rows) return hipSuccess;
-        ws.want(prefix_bytes + (parts * sizeof(float2) + 15) / 16 * 16 + parts * kD * sizeof(float));
+        ws.want(cross_bytes + (parts * sizeof(float2) + 15) / 16 * 16 + parts * kD * sizeof(float));
         return hipSuccess;
     }
     uint8_t* at = short_rows ? nullptr : static_cast<uint8_t*>(ws.ptr);
     A.groups = at ? (int)groups : 0;
-    A.prefix = reinterpret_cast<int32_t*>(at);
-    A.part_ml = reinterpret_cast<float2*>(at + prefix_bytes);
-    A.part_o = reinterpret_cast<float*>(at + prefix_bytes + (parts * sizeof(float2) + 15) / 16 * 16);
+    A.cross = reinterpret_cast<int4*>(at);
+    A.part_ml = reinterpret_cast<float2*>(at + cross_bytes);
+    A.part_o = reinterpret_cast<float*>(at + cross_bytes + (parts * sizeof(float2) + 15) / 16 * 16);
     const int64_t grid = at ? groups : rows;
     const size_t lds = kWaves * (kWaveLds + (size_t)A.per_chunk * kPart * sizeof(float));
     const auto kernel = A.per_chunk <= 4 ? paged_attn_kernel<1> : A.per_chunk <= 8 ? paged_attn_kernel<2> : paged_attn_kernel<4>;
     kernel<<<dim3((unsigned)grid), dim3(kThreads), lds, stream>>>(A);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !at) return e;
-    paged_join_kernel<<<dim3((unsigned)rows, (unsigned)A.per_chunk), dim3(kJoin), 0, stream>>>(A);
+    paged_join_kernel<<<dim3((unsigned)(groups - 1 + count), (unsigned)A.per_chunk), dim3(kJoin), 0, stream>>>(A);
     return hipGetLastError();
 }
 
