@@ -335,14 +335,23 @@ def dequantize(codes, scales, zeros, N: int, K: int, group: int = 128, bits: int
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 
 
+def _raw_stream(index):
+    """Handle of the current stream of GPU `index`.  (torch's own call for it
+    costs 0.1 us, a Stream object 2.8 us: more than a launch.)"""
+    import torch
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(index) if get is not None else torch.cuda.current_stream(index).cuda_stream
+
+
 def _launch(where, device, fn, *args):
     """fn(*args, stream) on `device` and its current stream."""
     import torch
-    if torch.cuda.current_device() == device.index:
-        st = fn(*args, torch.cuda.current_stream().cuda_stream)
+    index = device.index
+    if torch.cuda.current_device() == index:
+        st = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            st = fn(*args, torch.cuda.current_stream().cuda_stream)
+            st = fn(*args, _raw_stream(index))
     if st:
         check(st, where)
 

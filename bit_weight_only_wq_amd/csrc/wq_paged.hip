@@ -52,51 +52,61 @@ __device__ __forceinline__ void encode8(const uint4& u, const float4 (&h)[8], ui
 
 __device__ __forceinline__ float4 header4(const GroupHeader& g) { return make_float4(g.s, g.rcp, g.Z, g.thr); }
 
+__device__ __forceinline__ uint32_t pk_min(uint32_t a, uint32_t b) {
+    return as_u32(__builtin_elementwise_min(as_h2(a), as_h2(b)));
+}
+__device__ __forceinline__ uint32_t pk_max(uint32_t a, uint32_t b) {
+    return as_u32(__builtin_elementwise_max(as_h2(a), as_h2(b)));
+}
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_u(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+}
+
 // One side of one block by the 256 threads: thread (c8, r) = (tid % 16, tid / 16)
-// takes channels 8 c8 .. + 7 of eight tokens, 16 bytes each, so a load
-// instruction of a wave reads whole 256-byte token rows.  row(t) is the
-// address of token t's 128 channels.
+// holds channels 8 c8 .. + 7 of eight tokens, 16 bytes each, so a load
+// instruction of a wave reads whole 256-byte token rows.  Minima and maxima are
+// taken on pairs of fp16 values, as they lie.
 //
 // K (a group is a channel): tokens r + 16 i.  The channel's minimum and maximum
 // over the thread's tokens, then over r (lanes 16 and 32 apart, and the four
 // waves through LDS); 128 threads make the headers; eight codes are four bytes
 // of a token's code row, stored as they are.
-template <class Row>
-__device__ __forceinline__ void quantize_k(uint8_t* rec, const Row& row, float4* hdr, float (*mnx)[2][kD]) {
+__device__ __forceinline__ void quantize_k(uint8_t* rec, const uint4 (&u)[8], float4* hdr, uint32_t (*mnx)[2][kD / 2]) {
     const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
     const int c8 = tid & 15, r = tid >> 4;
-    uint4 u[8];
+    uint32_t mn[4] = {u[0].x, u[0].y, u[0].z, u[0].w}, mx[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) u[i] = *reinterpret_cast<const uint4*>(row(r + 16 * i) + 8 * c8);
+    for (int i = 1; i < 8; ++i) {
+        const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        float mn = __builtin_huge_valf(), mx = -__builtin_huge_valf();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-            const float x = half_bits_to_float((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
-            mn = __builtin_fminf(mn, x);
-            mx = __builtin_fmaxf(mx, x);
+        for (int e = 0; e < 4; ++e) {
+            mn[e] = pk_min(mn[e], w[e]);
+            mx[e] = pk_max(mx[e], w[e]);
         }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
 #pragma unroll
         for (int o = 16; o < 64; o <<= 1) {
-            mn = __builtin_fminf(mn, __shfl_xor(mn, o, 64));
-            mx = __builtin_fmaxf(mx, __shfl_xor(mx, o, 64));
+            mn[e] = pk_min(mn[e], (uint32_t)__shfl_xor((int)mn[e], o, 64));
+            mx[e] = pk_max(mx[e], (uint32_t)__shfl_xor((int)mx[e], o, 64));
         }
-        if (lane < 16) {
-            mnx[wv][0][8 * c8 + e] = mn;
-            mnx[wv][1][8 * c8 + e] = mx;
-        }
+    }
+    if (lane < 16) {
+        *reinterpret_cast<uint4*>(&mnx[wv][0][4 * c8]) = make_uint4(mn[0], mn[1], mn[2], mn[3]);
+        *reinterpret_cast<uint4*>(&mnx[wv][1][4 * c8]) = make_uint4(mx[0], mx[1], mx[2], mx[3]);
     }
     __syncthreads();
     if (tid < kD) {
-        float mn = mnx[0][0][tid], mx = mnx[0][1][tid];
+        uint32_t lo = mnx[0][0][tid >> 1], hi = mnx[0][1][tid >> 1];
 #pragma unroll
         for (int w = 1; w < 4; ++w) {
-            mn = __builtin_fminf(mn, mnx[w][0][tid]);
-            mx = __builtin_fmaxf(mx, mnx[w][1][tid]);
+            lo = pk_min(lo, mnx[w][0][tid >> 1]);
+            hi = pk_max(hi, mnx[w][1][tid >> 1]);
         }
-        const GroupHeader g = make_header(mn, mx, 15);
+        const int at = 16 * (tid & 1);
+        const GroupHeader g = make_header(half_bits_to_float((uint16_t)(lo >> at)), half_bits_to_float((uint16_t)(hi >> at)), 15);
         hdr[tid] = header4(g);
         reinterpret_cast<uint16_t*>(rec + kKScales)[tid] = g.sbits;
         reinterpret_cast<uint16_t*>(rec + kKZeros)[tid] = g.zbits;
@@ -119,32 +129,30 @@ __device__ __forceinline__ void quantize_k(uint8_t* rec, const Row& row, float4*
 // maximum over its 16 lanes; lanes 0..7 of the 16 make the eight headers; the
 // eight codes of one channel are four bytes of that channel's code row, turned
 // through an LDS tile so that rows are stored 16 bytes at a time.
-template <class Row>
-__device__ __forceinline__ void quantize_v(uint8_t* rec, const Row& row, float4* hdr, uint32_t* tile) {
+__device__ __forceinline__ void quantize_v(uint8_t* rec, const uint4 (&u)[8], float4* hdr, uint32_t* tile) {
     const int tid = threadIdx.x;
     const int c8 = tid & 15, r = tid >> 4;
-    uint4 u[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) u[i] = *reinterpret_cast<const uint4*>(row(8 * r + i) + 8 * c8);
-    float mn_own = 0.0f, mx_own = 0.0f;
+    uint32_t own = 0;                      // minimum and maximum of the lane's token (c8 < 8)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-        float mn = __builtin_huge_valf(), mx = -__builtin_huge_valf();
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float x = half_bits_to_float((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
-            mn = __builtin_fminf(mn, x);
-            mx = __builtin_fmaxf(mx, x);
-        }
-        group_minmax<16>(mn, mx);
-        if (c8 == i) {
-            mn_own = mn;
-            mx_own = mx;
-        }
+        uint32_t mn = pk_min(pk_min(w[0], w[1]), pk_min(w[2], w[3]));
+        uint32_t mx = pk_max(pk_max(w[0], w[1]), pk_max(w[2], w[3]));
+        // The halves against each other, then the 16 lanes: (min, max) in one word.
+        mn = pk_min(mn, __builtin_amdgcn_alignbit(mn, mn, 16));
+        mx = pk_max(mx, __builtin_amdgcn_alignbit(mx, mx, 16));
+        mn = pk_min(mn, dpp_u<0xB1>(mn));
+        mx = pk_max(mx, dpp_u<0xB1>(mx));
+        mn = pk_min(mn, dpp_u<0x4E>(mn));
+        mx = pk_max(mx, dpp_u<0x4E>(mx));
+        mn = pk_min(mn, dpp_u<0x141>(mn));
+        mx = pk_max(mx, dpp_u<0x141>(mx));
+        mn = pk_min(mn, dpp_u<0x140>(mn));
+        mx = pk_max(mx, dpp_u<0x140>(mx));
+        if (c8 == i) own = (mn & 0xFFFFu) | (mx << 16);
     }
     if (c8 < 8) {
-        const GroupHeader g = make_header(mn_own, mx_own, 15);
+        const GroupHeader g = make_header(half_bits_to_float((uint16_t)own), half_bits_to_float((uint16_t)(own >> 16)), 15);
         hdr[8 * r + c8] = header4(g);
         reinterpret_cast<uint16_t*>(rec + kVScales)[8 * r + c8] = g.sbits;
         reinterpret_cast<uint16_t*>(rec + kVZeros)[8 * r + c8] = g.zbits;
@@ -183,7 +191,7 @@ __global__ __launch_bounds__(kThreads) void paged_append_kernel(const AppendArgs
     __shared__ float4 hdr[kG];
     __shared__ __align__(16) uint32_t buf[kD * 17];
     __shared__ int found[4];
-    static_assert(sizeof(float) * 4 * 2 * kD <= sizeof(uint32_t) * kD * 17, "min/max fit in the tile");
+    static_assert(4 * 2 * (kD / 2) <= kD * 17, "minima and maxima fit in the tile");
 
     const int tid = threadIdx.x;
     const int64_t task = blockIdx.x, head = blockIdx.y;
@@ -212,30 +220,37 @@ __global__ __launch_bounds__(kThreads) void paged_append_kernel(const AppendArgs
     if (block * kG >= len) return;
     const bool first = task == first_task, whole = (block + 1) * kG <= len;
     if (!whole && !first) return;          // the first block's task writes the rows of the last
+    const uint16_t* in = side == 0 ? A.k : A.v;
+    const int64_t stride = side == 0 ? A.k_stride : A.v_stride;
+    uint16_t* win = window_of(A.c, slot, head, side);
+    // What is needed from memory is asked for at once: the block's rows, its page
+    // and the slots named before.
+    uint4 u[8];
+    int64_t page = -1;
+    if (whole) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = tid >> 4;
+            const int64_t p = block * kG + (side == 0 ? r + 16 * i : 8 * r + i);
+            u[i] = *reinterpret_cast<const uint4*>((p < start ? win + p % kG * kD : in + (cu0 + p - start) * stride + head * kD) +
+                                                   8 * (tid & 15));
+        }
+        page = A.c.table[slot * A.c.max_pages + block];
+    }
     if (A.seqs) {                          // a slot named twice: its first entry counts
         int again = 0;
         for (int64_t i = tid; i < entry; i += kThreads) again |= A.seqs[i] == slot;
         if (__syncthreads_or(again)) return;
     }
-
-    const uint16_t* in = side == 0 ? A.k : A.v;
-    const int64_t stride = side == 0 ? A.k_stride : A.v_stride;
-    uint16_t* win = window_of(A.c, slot, head, side);
-    if (whole) {
-        const int64_t page = A.c.table[slot * A.c.max_pages + block];
-        if (page >= 0 && page < A.c.num_pages) {
-            const auto row = [&](int t) -> const uint16_t* {
-                const int64_t p = block * kG + t;
-                return p < start ? win + t * kD : in + (cu0 + p - start) * stride + head * kD;
-            };
-            uint8_t* rec = record(A.c, page, head);
-            if (side == 0) quantize_k(rec, row, hdr, reinterpret_cast<float(*)[2][kD]>(buf));
-            else quantize_v(rec, row, hdr, buf);
-        }
+    if (page >= 0 && page < A.c.num_pages) {
+        uint8_t* rec = record(A.c, page, head);
+        if (side == 0) quantize_k(rec, u, hdr, reinterpret_cast<uint32_t(*)[2][kD / 2]>(buf));
+        else quantize_v(rec, u, hdr, buf);
     }
     if (!first || len % kG == 0) return;
-    // Rows of the last, unfinished block.  (quantize_* have read the old rows
-    // before their first barrier.)
+    // Rows of the last, unfinished block.  No thread overwrites a row that
+    // another has yet to read: a block quantized above has passed a barrier
+    // after its rows were used, and one without a page needs none of them.
     const int64_t tail = len / kG * kG, from = start > tail ? start : tail;
     for (int64_t i = tid; i < (len - from) * 16; i += kThreads) {
         const int64_t p = from + (i >> 4);
