@@ -687,7 +687,7 @@ wq_status wq_kv_paged_append(const void* k, const void* v, int64_t tokens, int64
     if (!aligned(k, 16) || !aligned(v, 16) || k_stride % 8 != 0 || v_stride % 8 != 0 || !aligned(cu, 4))
         return fail(WQ_ERR_MISALIGNED, "wq_kv_paged_append: k, v and their strides need 16-byte, cu 4-byte alignment");
     return check_hip(wq::launch_paged_append(k, v, tokens, k_stride, v_stride, a, lens, seqs, cu, count,
-                                             static_cast<hipStream_t>(stream)),
+                                             num_cus(), static_cast<hipStream_t>(stream)),
                      "wq_kv_paged_append launch");
 }
 

@@ -187,7 +187,7 @@ struct PagedArgs {
 constexpr int kPairsPerLaunch = 448;
 hipError_t launch_paged_append(const void* k, const void* v, int64_t tokens, int64_t k_stride, int64_t v_stride,
                                const PagedArgs& c, const int32_t* lens, const int32_t* seqs, const int32_t* cu,
-                               int64_t count, hipStream_t stream);
+                               int64_t count, int num_cus, hipStream_t stream);
 hipError_t launch_paged_attention(const void* q, int64_t q_stride, int64_t q_heads, const PagedArgs& c,
                                   const int32_t* lens, const int32_t* seqs, int64_t count, int64_t window,
                                   float scale, void* out, int64_t out_stride, int num_cus, const Scratch& ws,

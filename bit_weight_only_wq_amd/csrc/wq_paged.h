@@ -15,6 +15,18 @@ constexpr int kRecord = 17408;      // bytes of one page's record of one head
 constexpr int kVCodes = 8192, kKScales = 16384, kKZeros = 16640, kVScales = 16896, kVZeros = 17152;
 constexpr int kSide = kG * kD;      // fp16 elements of one side of a window
 
+// Asks for all of a kernel's arguments at its start.  They lie in host memory,
+// 64 bytes a line; left to the compiler each line is read where its first value
+// is used, and every such read is a trip of a microsecond or two on the path of
+// a short kernel.
+template <class T>
+__device__ __forceinline__ void read_arguments(const T& a) {
+    static_assert(sizeof(T) <= 4 * 64, "four lines");
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&a);
+    constexpr int n = sizeof(T) / 4;
+    asm volatile("" ::"s"(w[0]), "s"(w[n > 16 ? 16 : 0]), "s"(w[n > 32 ? 32 : 0]), "s"(w[n > 48 ? 48 : 0]), "s"(w[n - 1]));
+}
+
 // Slot of entry i, or -1 for padding.
 __device__ __forceinline__ int64_t slot_of(const PagedArgs& c, const int32_t* seqs, int64_t i) {
     const int64_t s = seqs ? seqs[i] : i;

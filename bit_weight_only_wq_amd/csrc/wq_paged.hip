@@ -28,118 +28,171 @@ struct AppendArgs {
     int64_t count;
 };
 
-// Codes of eight fp16 values of groups with header h[i] (s, 1/s, z, tie
-// threshold): the fp32 estimate round(x / s), or the exact decision where a
-// lane of the wave is too near a tie.
-__device__ __forceinline__ void encode8(const uint4& u, const float4 (&h)[8], uint32_t (&q)[8]) {
+// What encoding needs of a group: 1 / s, kRound + Z, s and s / 2.  Adding kRound
+// = 1.5 * 2^23 to a number of small magnitude rounds it to the nearest integer,
+// ties to even, and leaves that in the low bits.
+constexpr float kRound = 12582912.0f;
+__device__ __forceinline__ float4 header4(const GroupHeader& g) { return make_float4(g.rcp, kRound + g.Z, g.s, 0.5f * g.s); }
+
+// Eight 4-bit codes, of consecutive fp16 values in u whose groups' headers are
+// h(e), as the nibbles 0 .. 7 of a word.  Six instructions a value:
+// y = x / s + Z + kRound by one fma from fp16 x, which is k + Z + kRound with k
+// the nearest integer to x / s but for the reciprocal's error; r = x - k s, which
+// is exact, and |r| < s / 2 says that k is right; the clamp to 0 .. 15; and a
+// shift-and-add that leaves the constant part of each y in the word (kRound's
+// bits, 0x4B400000 at nibble e: their sum is taken off at the end, modulo 2^32).
+// Where a lane of the wave has |r| >= s / 2 (ties mostly: x = s / 2 is one value
+// in some thousands), k moves towards r unless it is a tie and k is even.
+template <class Head>
+__device__ __forceinline__ uint32_t encode8(const uint4& u, const Head& h) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    float x[8], k[8];
+    float y[8], r[8];
     bool near = false;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        x[i] = half_bits_to_float((uint16_t)(w[i >> 1] >> (16 * (i & 1))));
-        const float t = x[i] * h[i].y;
-        k[i] = __builtin_rintf(t);
-        near |= __builtin_fabsf(t - k[i]) > h[i].w;
+    for (int e = 0; e < 8; ++e) {
+        const float4 he = h(e);
+        const float x = (float)as_h2(w[e >> 1])[e & 1];
+        y[e] = __builtin_fmaf(x, he.x, he.y);
+        r[e] = __builtin_fmaf(he.y - y[e], he.z, x);
+        near |= __builtin_fabsf(r[e]) >= he.w;
     }
     if (__builtin_amdgcn_ballot_w64(near) != 0) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) k[i] = rne_div_exact(x[i], h[i].x, h[i].y, -h[i].z - 2.0f, 17.0f - h[i].z);
+        for (int e = 0; e < 8; ++e) {
+            const float4 he = h(e);
+            const float k = y[e] - he.y, a = __builtin_fabsf(r[e]);
+            const bool odd = __builtin_bit_cast(uint32_t, k + kRound) & 1u;
+            if (a > he.w || (a == he.w && odd)) y[e] += __builtin_copysignf(1.0f, r[e]);
+        }
     }
+    uint32_t q = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = (uint32_t)__builtin_amdgcn_fmed3f(k[i] + h[i].z, 0.0f, 15.0f);
+    for (int e = 7; e >= 0; --e)
+        q = (q << 4) + __builtin_bit_cast(uint32_t, __builtin_amdgcn_fmed3f(y[e], kRound, kRound + 15.0f));
+    // 0x4B400000 * (1 + 16 + 16^2 + ..), modulo 2^32.
+    return q - 0x4B400000u * 0x11111111u;
 }
 
-__device__ __forceinline__ float4 header4(const GroupHeader& g) { return make_float4(g.s, g.rcp, g.Z, g.thr); }
-
+// (As instructions: the compiler would first quiet NaNs, which do not occur.)
 __device__ __forceinline__ uint32_t pk_min(uint32_t a, uint32_t b) {
-    return as_u32(__builtin_elementwise_min(as_h2(a), as_h2(b)));
+    uint32_t r;
+    asm("v_pk_min_f16 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
 }
 __device__ __forceinline__ uint32_t pk_max(uint32_t a, uint32_t b) {
-    return as_u32(__builtin_elementwise_max(as_h2(a), as_h2(b)));
+    uint32_t r;
+    asm("v_pk_max_f16 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
 }
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_u(uint32_t v) {
     return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
 }
 
-// One side of one block by the 256 threads: thread (c8, r) = (tid % 16, tid / 16)
-// holds channels 8 c8 .. + 7 of eight tokens, 16 bytes each, so a load
-// instruction of a wave reads whole 256-byte token rows.  Minima and maxima are
-// taken on pairs of fp16 values, as they lie.
+// A quarter of one block of one head by 256 threads: part 0 and 1 are channels 0
+// .. 63 and 64 .. 127 of K, part 2 and 3 tokens 0 .. 63 and 64 .. 127 of V.  A
+// thread holds 16-byte pieces (eight channels) of four tokens.  Minima and
+// maxima are taken on pairs of fp16 values, as they lie.
 //
-// K (a group is a channel): tokens r + 16 i.  The channel's minimum and maximum
-// over the thread's tokens, then over r (lanes 16 and 32 apart, and the four
-// waves through LDS); 128 threads make the headers; eight codes are four bytes
-// of a token's code row, stored as they are.
-__device__ __forceinline__ void quantize_k(uint8_t* rec, const uint4 (&u)[8], float4* hdr, uint32_t (*mnx)[2][kD / 2]) {
-    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-    const int c8 = tid & 15, r = tid >> 4;
-    uint32_t mn[4] = {u[0].x, u[0].y, u[0].z, u[0].w}, mx[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
-#pragma unroll
-    for (int i = 1; i < 8; ++i) {
-        const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            mn[e] = pk_min(mn[e], w[e]);
-            mx[e] = pk_max(mx[e], w[e]);
-        }
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-#pragma unroll
-        for (int o = 16; o < 64; o <<= 1) {
-            mn[e] = pk_min(mn[e], (uint32_t)__shfl_xor((int)mn[e], o, 64));
-            mx[e] = pk_max(mx[e], (uint32_t)__shfl_xor((int)mx[e], o, 64));
-        }
-    }
-    if (lane < 16) {
-        *reinterpret_cast<uint4*>(&mnx[wv][0][4 * c8]) = make_uint4(mn[0], mn[1], mn[2], mn[3]);
-        *reinterpret_cast<uint4*>(&mnx[wv][1][4 * c8]) = make_uint4(mx[0], mx[1], mx[2], mx[3]);
-    }
-    __syncthreads();
-    if (tid < kD) {
-        uint32_t lo = mnx[0][0][tid >> 1], hi = mnx[0][1][tid >> 1];
-#pragma unroll
-        for (int w = 1; w < 4; ++w) {
-            lo = pk_min(lo, mnx[w][0][tid >> 1]);
-            hi = pk_max(hi, mnx[w][1][tid >> 1]);
-        }
-        const int at = 16 * (tid & 1);
-        const GroupHeader g = make_header(half_bits_to_float((uint16_t)(lo >> at)), half_bits_to_float((uint16_t)(hi >> at)), 15);
-        hdr[tid] = header4(g);
-        reinterpret_cast<uint16_t*>(rec + kKScales)[tid] = g.sbits;
-        reinterpret_cast<uint16_t*>(rec + kKZeros)[tid] = g.zbits;
-    }
-    __syncthreads();
-    float4 h[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) h[e] = hdr[8 * c8 + e];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        uint32_t q[8], w = 0;
-        encode8(u[i], h, q);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w |= q[e] << (4 * e);
-        *reinterpret_cast<uint32_t*>(rec + (r + 16 * i) * kRow + 4 * c8) = w;
-    }
+// K (a group is a channel): thread (c8, r) = (tid % 8, tid / 8) has tokens r +
+// 32 i.  The channel's minimum and maximum over the thread's tokens, then over r
+// (lanes 8, 16 and 32 apart, and the four waves through LDS); 64 threads make
+// the headers; eight codes are four bytes of a token's code row.
+// V (a group is a token): thread (c8, r) = (tid % 16, tid / 16) has tokens 4 r ..
+// 4 r + 3.  The token's minimum and maximum over its 16 lanes, of which four
+// make the headers; the four codes of one channel are two bytes of that
+// channel's code row, turned through an LDS tile so that rows are stored 16
+// bytes at a time.
+constexpr int kRows = 4;                   // tokens of a thread
+constexpr int kHalf = 64;                  // channels (K) or tokens (V) of a part
+constexpr int kTileRow = 9;                // words of a tile row: 32 bytes of codes, and one to spread the banks
+
+// Barrier for what the workgroup shares in LDS: it does not wait for loads and
+// stores of memory, as __syncthreads does.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// V (a group is a token): tokens 8 r .. 8 r + 7.  The token's minimum and
-// maximum over its 16 lanes; lanes 0..7 of the 16 make the eight headers; the
-// eight codes of one channel are four bytes of that channel's code row, turned
-// through an LDS tile so that rows are stored 16 bytes at a time.
-__device__ __forceinline__ void quantize_v(uint8_t* rec, const uint4 (&u)[8], float4* hdr, uint32_t* tile) {
+struct PartLds {
+    float4 hdr[kHalf];
+    uint32_t mnx[kThreads / 64][2][kHalf / 2];
+    uint32_t tile[kD * kTileRow];
+};
+
+// Token (of the block) and byte (of its 256) of the thread's piece i.
+__device__ __forceinline__ int part_token(int part, int i) {
     const int tid = threadIdx.x;
-    const int c8 = tid & 15, r = tid >> 4;
-    uint32_t own = 0;                      // minimum and maximum of the lane's token (c8 < 8)
+    return part < 2 ? (tid >> 3) + 32 * i : kHalf * (part & 1) + kRows * (tid >> 4) + i;
+}
+__device__ __forceinline__ int part_channel(int part) {
+    const int tid = threadIdx.x;
+    return part < 2 ? kHalf * part + 8 * (tid & 7) : 8 * (tid & 15);
+}
+
+__device__ __forceinline__ void quantize_part(uint8_t* rec, int part, const uint4 (&u)[kRows], PartLds& s) {
+    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, half = part & 1;
+    if (part < 2) {
+        const int c8 = tid & 7, r = tid >> 3;
+        uint32_t mn[4] = {u[0].x, u[0].y, u[0].z, u[0].w}, mx[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-        uint32_t mn = pk_min(pk_min(w[0], w[1]), pk_min(w[2], w[3]));
-        uint32_t mx = pk_max(pk_max(w[0], w[1]), pk_max(w[2], w[3]));
-        // The halves against each other, then the 16 lanes: (min, max) in one word.
-        mn = pk_min(mn, __builtin_amdgcn_alignbit(mn, mn, 16));
+        for (int i = 1; i < kRows; ++i) {
+            const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                mn[e] = pk_min(mn[e], w[e]);
+                mx[e] = pk_max(mx[e], w[e]);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            mn[e] = pk_min(mn[e], dpp_u<0x128>(mn[e]));       // row_ror 8
+            mx[e] = pk_max(mx[e], dpp_u<0x128>(mx[e]));
+#pragma unroll
+            for (int o = 16; o < 64; o <<= 1) {
+                mn[e] = pk_min(mn[e], (uint32_t)__shfl_xor((int)mn[e], o, 64));
+                mx[e] = pk_max(mx[e], (uint32_t)__shfl_xor((int)mx[e], o, 64));
+            }
+        }
+        if (lane < 8) {
+            *reinterpret_cast<uint4*>(&s.mnx[wv][0][4 * c8]) = make_uint4(mn[0], mn[1], mn[2], mn[3]);
+            *reinterpret_cast<uint4*>(&s.mnx[wv][1][4 * c8]) = make_uint4(mx[0], mx[1], mx[2], mx[3]);
+        }
+        lds_barrier();
+        GroupHeader g;
+        if (tid < kHalf) {
+            uint32_t lo = s.mnx[0][0][tid >> 1], hi = s.mnx[0][1][tid >> 1];
+#pragma unroll
+            for (int w = 1; w < kThreads / 64; ++w) {
+                lo = pk_min(lo, s.mnx[w][0][tid >> 1]);
+                hi = pk_max(hi, s.mnx[w][1][tid >> 1]);
+            }
+            const int at = 16 * (tid & 1);
+            g = make_header(half_bits_to_float((uint16_t)(lo >> at)), half_bits_to_float((uint16_t)(hi >> at)), 15);
+            s.hdr[tid] = header4(g);
+        }
+        lds_barrier();
+        float4 h[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[e] = s.hdr[8 * c8 + e];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+            *reinterpret_cast<uint32_t*>(rec + (r + 32 * i) * kRow + half * (kRow / 2) + 4 * c8) =
+                encode8(u[i], [&](int e) { return h[e]; });
+        if (tid < kHalf) {
+            reinterpret_cast<uint16_t*>(rec + kKScales)[kHalf * half + tid] = g.sbits;
+            reinterpret_cast<uint16_t*>(rec + kKZeros)[kHalf * half + tid] = g.zbits;
+        }
+        return;
+    }
+    const int c8 = tid & 15, r = tid >> 4;
+    uint32_t own = 0;                      // minimum and maximum of the lane's token (c8 < 4)
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        uint32_t mn = pk_min(pk_min(u[i].x, u[i].y), pk_min(u[i].z, u[i].w));
+        uint32_t mx = pk_max(pk_max(u[i].x, u[i].y), pk_max(u[i].z, u[i].w));
+        mn = pk_min(mn, __builtin_amdgcn_alignbit(mn, mn, 16));   // the halves against each other, then the lanes
         mx = pk_max(mx, __builtin_amdgcn_alignbit(mx, mx, 16));
         mn = pk_min(mn, dpp_u<0xB1>(mn));
         mx = pk_max(mx, dpp_u<0xB1>(mx));
@@ -151,51 +204,52 @@ __device__ __forceinline__ void quantize_v(uint8_t* rec, const uint4 (&u)[8], fl
         mx = pk_max(mx, dpp_u<0x140>(mx));
         if (c8 == i) own = (mn & 0xFFFFu) | (mx << 16);
     }
-    if (c8 < 8) {
-        const GroupHeader g = make_header(half_bits_to_float((uint16_t)own), half_bits_to_float((uint16_t)(own >> 16)), 15);
-        hdr[8 * r + c8] = header4(g);
-        reinterpret_cast<uint16_t*>(rec + kVScales)[8 * r + c8] = g.sbits;
-        reinterpret_cast<uint16_t*>(rec + kVZeros)[8 * r + c8] = g.zbits;
+    GroupHeader g;
+    if (c8 < kRows) {
+        g = make_header(half_bits_to_float((uint16_t)own), half_bits_to_float((uint16_t)(own >> 16)), 15);
+        s.hdr[kRows * r + c8] = header4(g);
     }
-    __syncthreads();
-    uint32_t w[8] = {};                    // channel e of the thread: tokens 8 r + i in nibble i
+    lds_barrier();
+    uint32_t q[kRows];                     // token 4 r + i: the thread's eight channels in the nibbles
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float4 ht = hdr[8 * r + i];
-        const float4 h[8] = {ht, ht, ht, ht, ht, ht, ht, ht};
-        uint32_t q[8];
-        encode8(u[i], h, q);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] |= q[e] << (4 * i);
+    for (int i = 0; i < kRows; ++i) {
+        const float4 h = s.hdr[kRows * r + i];
+        q[i] = encode8(u[i], [&](int) { return h; });
     }
-    // Row stride of 17 words: the 16 rows a store instruction meets fall on
-    // different banks.
+    uint16_t* to = reinterpret_cast<uint16_t*>(s.tile);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) tile[(8 * c8 + e) * 17 + r] = w[e];
-    __syncthreads();
+    for (int e = 0; e < 8; ++e) {
+        uint32_t w = 0;                    // channel e: tokens 4 r + i in nibble i
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int at = tid + kThreads * i, d = at >> 2, q4 = (at & 3) * 4;
-        const uint32_t* s = tile + d * 17 + q4;
-        *reinterpret_cast<uint4*>(rec + kVCodes + d * kRow + 4 * q4) = make_uint4(s[0], s[1], s[2], s[3]);
+        for (int i = 0; i < kRows; ++i) w |= ((q[i] >> (4 * e)) & 15u) << (4 * i);
+        to[(8 * c8 + e) * (2 * kTileRow) + r] = (uint16_t)w;
+    }
+    lds_barrier();
+    const int d = tid >> 1, q4 = (tid & 1) * 4;
+    const uint32_t* w = s.tile + d * kTileRow + q4;
+    *reinterpret_cast<uint4*>(rec + kVCodes + d * kRow + half * (kRow / 2) + 4 * q4) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (c8 < kRows) {
+        reinterpret_cast<uint16_t*>(rec + kVScales)[kHalf * half + kRows * r + c8] = g.sbits;
+        reinterpret_cast<uint16_t*>(rec + kVZeros)[kHalf * half + kRows * r + c8] = g.zbits;
     }
 }
 
-// Grid (tasks, heads, sides).  A task is one block of one entry; entry i has
-// the tasks from cu[i] / 128 + 2 i on, which leaves room for every block it
-// can touch (n tokens touch at most n / 128 + 2), so a task finds its entry by
+// Grid (tasks, heads, parts).  A task is one block of one entry; entry i has the
+// tasks from cu[i] / 128 + 2 i on, which leaves room for every block it can
+// touch (n tokens touch at most n / 128 + 2), so a task finds its entry by
 // counting, without a running sum.  The task of an entry's first block also
-// writes the window's new rows, after it has read the old ones; so no other
-// workgroup writes what it reads.
+// writes the window's new rows (each part the channels or, of V, the rows it
+// reads of an old window: part p of a side its 64 channels), after it has read
+// the old ones; so no other workgroup writes what it reads.
 __global__ __launch_bounds__(kThreads) void paged_append_kernel(const AppendArgs A) {
-    __shared__ float4 hdr[kG];
-    __shared__ __align__(16) uint32_t buf[kD * 17];
+    __shared__ __align__(16) PartLds s;
     __shared__ int found[4];
-    static_assert(4 * 2 * (kD / 2) <= kD * 17, "minima and maxima fit in the tile");
+    read_arguments(A);
 
     const int tid = threadIdx.x;
-    const int64_t task = blockIdx.x, head = blockIdx.y;
-    const int side = blockIdx.z;
+    const int64_t task = blockIdx.x;
+    const int part = blockIdx.z, side = part >> 1;
+    const int head = blockIdx.y;
     int64_t entry = task, cu0 = task, cu1 = task + 1, first_task = task;
     if (A.cu) {
         int before = 0;                    // entries whose tasks start at or before this one
@@ -222,18 +276,19 @@ __global__ __launch_bounds__(kThreads) void paged_append_kernel(const AppendArgs
     if (!whole && !first) return;          // the first block's task writes the rows of the last
     const uint16_t* in = side == 0 ? A.k : A.v;
     const int64_t stride = side == 0 ? A.k_stride : A.v_stride;
+    const int old = start > block * kG ? (int)(start - block * kG) : 0;        // rows of the block that the window holds
+    const uint16_t* block_in = in + (cu0 + block * kG - start) * stride;       // its row 0's place among the new ones
     uint16_t* win = window_of(A.c, slot, head, side);
     // What is needed from memory is asked for at once: the block's rows, its page
     // and the slots named before.
-    uint4 u[8];
+    uint4 u[kRows];
     int64_t page = -1;
     if (whole) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = tid >> 4;
-            const int64_t p = block * kG + (side == 0 ? r + 16 * i : 8 * r + i);
-            u[i] = *reinterpret_cast<const uint4*>((p < start ? win + p % kG * kD : in + (cu0 + p - start) * stride + head * kD) +
-                                                   8 * (tid & 15));
+        for (int i = 0; i < kRows; ++i) {
+            const int t = part_token(part, i);
+            u[i] = *reinterpret_cast<const uint4*>((t < old ? win + t * kD : block_in + t * stride + head * kD) +
+                                                   part_channel(part));
         }
         page = A.c.table[slot * A.c.max_pages + block];
     }
@@ -242,21 +297,98 @@ __global__ __launch_bounds__(kThreads) void paged_append_kernel(const AppendArgs
         for (int64_t i = tid; i < entry; i += kThreads) again |= A.seqs[i] == slot;
         if (__syncthreads_or(again)) return;
     }
-    if (page >= 0 && page < A.c.num_pages) {
-        uint8_t* rec = record(A.c, page, head);
-        if (side == 0) quantize_k(rec, u, hdr, reinterpret_cast<uint32_t(*)[2][kD / 2]>(buf));
-        else quantize_v(rec, u, hdr, buf);
-    }
+    if (page >= 0 && page < A.c.num_pages) quantize_part(record(A.c, page, head), part, u, s);
     if (!first || len % kG == 0) return;
-    // Rows of the last, unfinished block.  No thread overwrites a row that
-    // another has yet to read: a block quantized above has passed a barrier
-    // after its rows were used, and one without a page needs none of them.
+    // The new rows of the last, unfinished block: a part writes what it alone
+    // reads of an old window (K: its channels, V: its rows), which it has read:
+    // a block quantized above has passed a barrier after its rows were used, and
+    // one without a page needs none of them.
     const int64_t tail = len / kG * kG, from = start > tail ? start : tail;
-    for (int64_t i = tid; i < (len - from) * 16; i += kThreads) {
-        const int64_t p = from + (i >> 4);
-        const int c = (int)(i & 15) * 8;
-        *reinterpret_cast<uint4*>(win + (p - tail) * kD + c) =
-            *reinterpret_cast<const uint4*>(in + (cu0 + p - start) * stride + head * kD + c);
+    const int lo = part < 2 ? 0 : kHalf * (part & 1), hi = part < 2 ? kG : lo + kHalf;
+    const int r0 = (int)(from - tail) > lo ? (int)(from - tail) : lo, r1 = (int)(len - tail) < hi ? (int)(len - tail) : hi;
+    const int pieces = part < 2 ? 8 : 16, c0 = part < 2 ? kHalf * part : 0;
+    const uint16_t* tail_in = in + (cu0 + tail - start) * stride;
+    for (int i = tid; i < (r1 - r0) * pieces; i += kThreads) {
+        const int r = r0 + i / pieces, c = c0 + i % pieces * 8;
+        *reinterpret_cast<uint4*>(win + r * kD + c) = *reinterpret_cast<const uint4*>(tail_in + r * stride + head * kD + c);
+    }
+}
+
+// One token per entry, up to kMaxOnes entries: a few workgroups share out what
+// there is to do, since in most steps few entries fill a block, and the time of
+// a call is the time to start workgroups and to find those out.  Every workgroup
+// reads all slots and lengths; the parts of the blocks to quantize go round the
+// workgroups, and the rows to copy round the waves.
+constexpr int kMaxOnes = 1024;
+constexpr int kCopyHeads = 8;              // heads of a copying task
+
+__global__ __launch_bounds__(kThreads) void paged_append_ones_kernel(const AppendArgs A) {
+    __shared__ __align__(16) PartLds s;
+    __shared__ int slots[kMaxOnes], lens[kMaxOnes];   // of good entries; slot -1 otherwise
+    read_arguments(A);
+    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, count = (int)A.count;
+    for (int i = tid; i < (count + 63) / 64 * 64; i += kThreads) {
+        const int64_t slot = i < count ? slot_of(A.c, A.seqs, i) : -1;
+        const int64_t len = slot >= 0 ? A.lens[slot] : 0;
+        slots[i] = (int)slot;
+        lens[i] = len >= 1 && len <= capacity(A.c) ? (int)len : 0;
+    }
+    __syncthreads();
+    // A slot named twice: its first entry counts (whole wave; uniform).
+    const auto repeated = [&](int entry) {
+        const int slot = slots[entry];
+        bool again = false;
+        for (int i = lane; i < entry; i += 64) again |= slots[i] == slot;
+        return A.seqs && __builtin_amdgcn_ballot_w64(again) != 0;
+    };
+
+    // Blocks that become whole: quantizing tasks (which, head, part) in order.
+    const int per_block = (int)A.c.heads * 4;
+    int seen = 0;                          // whole blocks in the entries before
+    int64_t task = blockIdx.x;
+    for (int base = 0; base < count; base += 64) {
+        uint64_t whole = __builtin_amdgcn_ballot_w64(lens[base + lane] > 0 && lens[base + lane] % kG == 0);
+        const int here = __builtin_popcountll(whole);
+        for (; task < (int64_t)(seen + here) * per_block; task += gridDim.x) {
+            int k = (int)(task / per_block) - seen;
+            const int hp = (int)(task % per_block), head = hp >> 2, part = hp & 3, side = part >> 1;
+            uint64_t m = whole;
+            for (; k > 0; --k) m &= m - 1;
+            const int entry = base + __builtin_ctzll(m);
+            const int64_t slot = slots[entry], block = lens[entry] / kG - 1;
+            const uint16_t* win = window_of(A.c, slot, head, side);
+            const uint16_t* fresh = side == 0 ? A.k + entry * A.k_stride + head * kD : A.v + entry * A.v_stride + head * kD;
+            uint4 u[kRows];
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                const int t = part_token(part, i);
+                u[i] = *reinterpret_cast<const uint4*>((t < kG - 1 ? win + t * kD : fresh) + part_channel(part));
+            }
+            const int64_t page = A.c.table[slot * A.c.max_pages + block];
+            if (repeated(entry) || page < 0 || page >= A.c.num_pages) continue;
+            quantize_part(record(A.c, page, head), part, u, s);
+            lds_barrier();                 // the next task's use of s
+        }
+        seen += here;
+    }
+
+    // Rows that go to a window: tasks (entry, eight heads).
+    const int groups = ((int)A.c.heads + kCopyHeads - 1) / kCopyHeads;
+    const int waves = gridDim.x * (kThreads / 64);
+    for (int64_t t = (int64_t)blockIdx.x * (kThreads / 64) + wv; t < (int64_t)count * groups; t += waves) {
+        const int entry = (int)(t / groups), h0 = (int)(t % groups) * kCopyHeads;
+        const int len = lens[entry];
+        if (len == 0 || len % kG == 0 || repeated(entry)) continue;
+        const int nh = (int)A.c.heads - h0 < kCopyHeads ? (int)A.c.heads - h0 : kCopyHeads;
+        const int64_t slot = slots[entry];
+#pragma unroll
+        for (int i = 0; i < kCopyHeads * 2 * 16 / 64; ++i) {
+            const int at = lane + 64 * i, c = at % 16 * 8, side = at / 16 % 2, h = at / 32;
+            if (h < nh)
+                *reinterpret_cast<uint4*>(window_of(A.c, slot, h0 + h, side) + (len % kG - 1) * kD + c) =
+                    *reinterpret_cast<const uint4*>((side == 0 ? A.k + entry * A.k_stride : A.v + entry * A.v_stride) +
+                                                    (h0 + h) * kD + c);
+        }
     }
 }
 
@@ -446,11 +578,17 @@ __global__ __launch_bounds__(kThreads) void compact_move_kernel(const PagedArgs 
 
 hipError_t launch_paged_append(const void* k, const void* v, int64_t tokens, int64_t k_stride, int64_t v_stride,
                                const PagedArgs& c, const int32_t* lens, const int32_t* seqs, const int32_t* cu,
-                               int64_t count, hipStream_t stream) {
+                               int64_t count, int num_cus, hipStream_t stream) {
     const AppendArgs A{c, static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), tokens, k_stride,
                        v_stride, lens, seqs, cu, count};
+    if (!cu && count <= kMaxOnes) {
+        // As many workgroups as there can be tasks, up to two per compute unit.
+        const int64_t wgs = 4 * c.heads * count, most = 2 * (int64_t)num_cus;
+        paged_append_ones_kernel<<<dim3((unsigned)(wgs < most ? wgs : most)), dim3(kThreads), 0, stream>>>(A);
+        return hipGetLastError();
+    }
     const int64_t tasks = cu ? tokens / kG + 2 * count : count;
-    paged_append_kernel<<<dim3((unsigned)tasks, (unsigned)c.heads, 2), dim3(kThreads), 0, stream>>>(A);
+    paged_append_kernel<<<dim3((unsigned)tasks, (unsigned)c.heads, 4), dim3(kThreads), 0, stream>>>(A);
     return hipGetLastError();
 }
 

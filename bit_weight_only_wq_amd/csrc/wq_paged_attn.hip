@@ -225,6 +225,7 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
     extern __shared__ __align__(16) uint8_t lds[];
     __shared__ int chunk_units[kMaxCount / 64];
     __shared__ int seg_row[2 * kWaves], seg_begin[2 * kWaves], seg_end[2 * kWaves];   // (2 wave + 0 first, 1 last)
+    read_arguments(A);
     const int lane = threadIdx.x & 63, wv = uniform(threadIdx.x >> 6);
     const int g = lane >> 4, m = lane & 15;
     const int rows = (int)A.c.heads * A.chunks;                          // of an entry
@@ -900,6 +901,7 @@ __global__ __launch_bounds__(kJoin) void paged_join_kernel(const AttnArgs A) {
     constexpr int kWide = kJoin / (kD / 4);
     __shared__ f4_t acc[kWide][kD / 4];
     __shared__ float2 acc_rl[kWide];
+    read_arguments(A);
     const int rows = (int)A.c.heads * A.chunks, tid = threadIdx.x;
     if ((int)blockIdx.x >= A.groups - 1) {
         if (blockIdx.y != 0) return;
