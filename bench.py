@@ -23,6 +23,7 @@ sample of the same workload.
     python bench.py --sweep        # batch sweep across the ridge (K=N=8192), table only
     python bench.py --decode-set   # 7B-class decode step (224 products, B=32), table only
     python bench.py --kv           # decode attention over an int4 KV cache, table only
+    python bench.py --kv-paged     # decode step over a paged int4 KV cache: rope, append, attention, table only
     python bench.py --ceiling      # load-only probe read rates (and plain torch rates), table only
 """
 
@@ -57,6 +58,10 @@ def parse():
     p.add_argument("--kv", action="store_true",
                    help="decode attention over an int4 KV cache, 1024 heads x 4096 tokens "
                         "(a 7B-class model's whole cache; table line)")
+    p.add_argument("--kv-paged", action="store_true",
+                   help="decode step of one layer's attention over a paged int4 KV cache: rotary "
+                        "positions, append and attention of 64 sequences of about 4096 tokens, "
+                        "8 KV heads, 32 query heads (table line)")
     p.add_argument("--format", choices=["nf4", "offset"], default=None,
                    help="another weight format on the step's workload: NF4 at blocks of 64, or "
                         "the float-offset variant at the workload's group and --bits; quantize + "
@@ -115,6 +120,7 @@ KERNEL_SOURCES = {
 }
 KV_WORKLOAD = "kv_decode_7b_ctx4096"
 KV_SHAPE = (1024, 4096, 128, 128)   # heads (32 layers x 32), tokens, head dim, block
+KV_PAGED_SHAPE = (64, 8, 32, 4096)  # sequences, KV heads, query heads, tokens
 # rocprofv3 kernel-name fragment of each family.
 KERNEL_NAMES = {"gemv": "gemv_", "mfma": "gemm_mfma_kernel", "xr": "gemm_xr_kernel", "qs": "gemm_qs_kernel",
                 "q4": "gemm_q4_kernel", "ts": "gemm_ts_kernel", "sk": "gemm_sk_kernel", "kw": "gemm_kw_kernel",
@@ -774,6 +780,99 @@ def run_kv(args):
     return row
 
 
+def run_kv_paged(args, shape=KV_PAGED_SHAPE, layers=4):
+    """One layer's attention part of a decode step over a paged int4 cache: the
+    packed q, k, v row's q and k turned by their positions in place, k and v
+    appended, and the attention of every sequence.  Caches of `layers` layers
+    take turns (1.1 GB, beyond the 256 MB Infinity Cache).  The sequences'
+    lengths are spread over a block and grow by one each step, going back by a
+    block at its end, so on average one sequence in 128 completes a block per
+    step.  Pages lie in the pool in random order."""
+    import torch
+
+    import bit_weight_only_wq_amd as wq
+    from bit_weight_only_wq_amd import roofline as rl
+
+    S, H, HQ, T = shape
+    D = G = 128
+    nb = T // G
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    table = torch.randperm(S * nb, generator=gen, device="cuda").int().view(S, nb)
+    caches = [wq.PagedKV(H, S * nb, S, nb) for _ in range(layers)]
+    full = torch.full((S,), T, dtype=torch.int32, device="cuda")
+    cu = torch.arange(0, S * T + 1, T, dtype=torch.int32, device="cuda")
+    for cache in caches:
+        cache.table.copy_(table)
+        k = torch.randn((S * T, H, D), generator=gen, device="cuda", dtype=torch.float16)
+        k[:, :, 3] *= 8.0
+        wq.kv_paged_append(k, torch.randn((S * T, H, D), generator=gen, device="cuda", dtype=torch.float16), cache,
+                           full, cu=cu)
+    del k
+    freqs = wq.rope_frequencies(D)
+    phase = torch.arange(S, dtype=torch.int32, device="cuda") * G // S
+    lens = [T - G + 1 + (phase + s) % G for s in range(G)]
+    pos = [n - 1 for n in lens]
+    rows = [torch.randn((S, HQ + 2 * H, D), generator=gen, device="cuda", dtype=torch.float16) for _ in range(G)]
+    out = torch.empty((S, HQ, D), dtype=torch.float16, device="cuda")
+    ws = wq.kv_paged_workspace(caches[0], S, HQ)
+    stream = torch.cuda.current_stream()
+
+    def rope(i):
+        turned = rows[i % G][:, :HQ + H]
+        wq.rope(turned, pos[i % G], freqs, out=turned)
+
+    def append(i):
+        x = rows[i % G]
+        wq.kv_paged_append(x[:, HQ:HQ + H], x[:, HQ + H:], caches[i % layers], lens[i % G])
+
+    def attention(i):
+        wq.kv_paged_attention(rows[i % G][:, :HQ], caches[i % layers], lens[i % G], out=out, workspace=ws)
+
+    def step(i):
+        rope(i)
+        append(i)
+        attention(i)
+
+    def burst(fn):
+        for i in range(args.warmup):
+            fn(i)
+        torch.cuda.synchronize()
+        e0 = torch.cuda.Event(enable_timing=True)
+        e1 = torch.cuda.Event(enable_timing=True)
+        e0.record(stream)
+        for i in range(args.steps):
+            fn(args.warmup + i)
+        e1.record(stream)
+        torch.cuda.synchronize()
+        return e0.elapsed_time(e1) / args.steps
+
+    ms = burst(step)
+    timed = [lens[(args.warmup + i) % G] for i in range(args.steps)]
+    blocks = sum(int((n // G).sum()) for n in timed) / args.steps
+    rest = sum(int((n % G).sum()) for n in timed) / args.steps
+    done = sum(int((n % G == 0).sum()) for n in timed) / args.steps
+    nbytes = {"rope": 4 * S * (HQ + H) * D, "kv_paged_append": rl.kv_paged_append_bytes(H, S, done),
+              "kv_paged_attention": rl.kv_paged_attention_bytes(S, H, HQ, blocks, rest)}
+    kernels = {}
+    for name, fn in (("rope", rope), ("kv_paged_append", append), ("kv_paged_attention", attention)):
+        us = burst(fn) * 1e3
+        kernels[name] = {"avg_us": round(us, 2), "bytes": int(nbytes[name]),
+                         "achieved_GBps": round(nbytes[name] / us / 1e3, 1)}
+    total = sum(nbytes.values())
+    gbs = total / (ms * 1e-3) / 1e9
+    row = {"metric": "decode step over a paged int4 KV cache: rope, append, attention (GB/s)",
+           "value": round(gbs, 1), "unit": "GB/s", "n_gpus": 1, "steps": args.steps, "warmup": args.warmup,
+           "ms_per_step": round(ms, 4), "higher_is_better": True, "dtype": "f16", "data": "synthetic",
+           "config": {"workload": "kv_paged_decode", "sequences": S, "kv_heads": H, "q_heads": HQ, "tokens": T,
+                      "head_dim": D, "group": G, "bits": 4, "layers_in_turn": layers},
+           "roofline": {"bound": "hbm", "achieved": round(gbs, 1), "peak": rl.MI355X_HBM_BYTES_PER_S / 1e9,
+                        "unit": "GB/s", "frac": round(gbs * 1e9 / rl.MI355X_HBM_BYTES_PER_S, 4),
+                        "bytes_per_step": int(total)},
+           "kernels": kernels}
+    print(json.dumps(row), flush=True)
+    return row
+
+
 def run_format(args):
     """Another weight format on the step's workload: NF4 at blocks of 64 (the
     block the NF4 paragraph of "Gör inference billig" uses), or the
@@ -869,6 +968,9 @@ def main():
     if args.kv:
         run_kv(args)
         calibration_copy(args)
+        return
+    if args.kv_paged:
+        run_kv_paged(args)
         return
     if args.format:
         run_format(args)

@@ -406,6 +406,8 @@ def rope_frequencies(rot: int, base: float = 10000.0, kind: str = "none", factor
     if rot < 0 or rot % 2 or base <= 0 or factor <= 0 or kind not in ("none", "linear", "base", "parts"):
         raise ValueError(f"rope_frequencies: need even rot >= 0, base > 0, factor > 0 and a known kind (rot={rot} "
                          f"kind={kind!r})")
+    if kind == "parts" and not (context > 0 and low < high):
+        raise ValueError(f"rope_frequencies: need context > 0 and low < high (context={context} low={low} high={high})")
     if kind == "base" and rot > 2:
         base = base * factor ** (rot / (rot - 2))
     f = torch.pow(torch.tensor(base, dtype=torch.float64), -torch.arange(0, rot, 2, dtype=torch.float64) / max(rot, 1))

@@ -106,3 +106,17 @@ def kv_append_bytes(heads: int, group: int = 128, head_dim: int = 128) -> int:
     """Quantize-on-append of one block per head: fp16 K and V read, codes and
     headers written."""
     return 2 * 2 * heads * group * head_dim + kv_cache_bytes(heads, group, head_dim, group)
+
+
+def kv_paged_attention_bytes(rows: int, heads: int, q_heads: int, blocks: float, rest: float) -> float:
+    """Algorithmic bytes of one paged decode attention: `blocks` whole blocks (a
+    page record per KV head) and `rest` fp16 tokens of the windows read, summed
+    over the rows, the queries read and the outputs written."""
+    return heads * (blocks * 17408 + rest * 512) + 2 * 2 * rows * q_heads * 128
+
+
+def kv_paged_append_bytes(heads: int, tokens: int, done: float) -> float:
+    """One append of a token per row: fp16 k and v read and put into the windows;
+    of the `done` blocks that become whole, the windows' other tokens read and a
+    record written."""
+    return heads * (tokens * 4 * 256 + done * (127 * 512 + 17408))

@@ -510,7 +510,7 @@ wq_status wq_kv_paged_append(const void* k, const void* v, int64_t tokens, int64
  * q, out   fp16 [count][q_heads][128], q_stride and out_stride elements from
  *          one entry to the next (>= q_heads * 128); q 16-byte aligned with
  *          q_stride a multiple of 8, out 8-byte aligned with out_stride a
- *          multiple of 4
+ *          multiple of 4; out and q do not overlap
  * fp32 scores, softmax and sums.  Results do not depend on timing (no
  * atomics), but on the batch: the work of all entries is cut into equal parts,
  * and where a part ends inside a sequence, its sums are joined by a second

@@ -1,0 +1,111 @@
+"""The paged int4 KV cache at the sizes its kernels change their form: decode
+appends of more entries than one workgroup's list, repeated and padding slots
+among single tokens, pools past 4 GB, and the paged decode step of bench.py."""
+
+import sys
+from types import SimpleNamespace
+
+import numpy as np
+import pytest
+
+from conftest import ROOT
+from gpu_util import device, note, to_dev
+from paged_util import D, G, Host, append, draw_tokens, gpu_cache
+from test_gpu_paged import check_attention, i32
+
+import bit_weight_only_wq_amd as wq
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("count", [1, 63, 64, 65, 1024, 1025, 1500])
+def test_append_single_tokens_of_many_slots(count):
+    """One token each, a third of the slots completing a block."""
+    device()
+    rng = np.random.default_rng(count)
+    host = Host(1, count + 2, count, 1)
+    cache = gpu_cache(wq, host)
+    note(f"paged append {count} slots to near a block")
+    append(wq, cache, host, [(s, *draw_tokens(rng, 127 if s % 3 == 0 else 1, 1)) for s in range(count)])
+    note(f"paged append one token to each of {count} slots")
+    append(wq, cache, host, [(int(s), *draw_tokens(rng, 1, 1)) for s in rng.permutation(count)], cu=False)
+    host.check_buffers(cache, count)
+
+
+@pytest.mark.parametrize("count", [40, 1100])
+def test_append_single_tokens_left_out(count):
+    """Of single tokens: padding, a slot's second entry, an empty slot, a length
+    past the table and a whole block without a page leave all buffers alone."""
+    device()
+    rng = np.random.default_rng(77)
+    heads, S = 2, 8
+    host = Host(heads, 9, S, 2)
+    cache = gpu_cache(wq, host)
+    append(wq, cache, host, [(s, *draw_tokens(rng, 127, heads)) for s in range(6)])
+    K, V = draw_tokens(rng, count, heads)
+    seqs = np.full(count, -1, np.int32)
+    seqs[:9] = [3, 3, S, 0, 5, 6, 7, 0, 2 ** 31 - 1]
+    seqs[-1] = 4
+    lens = host.lens
+    lens[[0, 3, 4, 5]] += 1
+    lens[6], lens[7] = 0, 2 * G + 200
+    host.give_pages(0, 1)
+    host.give_pages(3, 1)
+    host.table[4, 0], host.table[5, 0] = 9, -1          # no such pages
+    cache.table.copy_(to_dev(host.table))
+    before_w, before_p = cache.windows.clone(), cache.pages.clone()
+    note(f"paged append single tokens left out, {count} entries")
+    wq.kv_paged_append(to_dev(K), to_dev(V), cache, to_dev(lens), seqs=to_dev(seqs))
+    host.add(3, K[:1], V[:1])
+    host.add(0, K[3:4], V[3:4])
+    want_p = before_p.clone()
+    for s in (0, 3):
+        want_p[host.table[s, 0]] = cache.pages[host.table[s, 0]]
+    assert torch.equal(cache.pages, want_p)
+    for s in (1, 2, 6, 7):
+        assert torch.equal(cache.windows[s], before_w[s]), s
+    host.K[4], host.V[4] = host.K[4][:0], host.V[4][:0]  # their blocks have no page to compare
+    host.K[5], host.V[5] = host.K[5][:0], host.V[5][:0]
+    host.check_buffers(cache, "left out")
+
+
+def test_pages_past_4_gb():
+    """Page ids whose byte offsets pass 2^31 and 2^32, in every operator."""
+    device()
+    heads, pages = 8, 31500                              # 139264 bytes a page, 4.39 GB
+    rng = np.random.default_rng(5)
+    host = Host(heads, pages, 3, 4)
+    ids = [pages - 1, 15421, 30841, 15420, 30840, 7, pages - 2, 2]     # about 2^31 and 2^32 bytes
+    host.free = ids[::-1]
+    cache = wq.PagedKV(heads, pages, 3, 4)
+    note("paged pool of 4.39 GB")
+    append(wq, cache, host, [(0, *draw_tokens(rng, 3 * G + 9, heads)), (1, *draw_tokens(rng, 2 * G, heads))])
+    q = rng.standard_normal((3, 2 * heads, D)).astype(np.float16)
+    for use_ws in (True, False):
+        out = wq.kv_paged_attention(to_dev(q), cache, to_dev(host.lens), use_workspace=use_ws)
+        check_attention(out, host, q, [0, 1, 2], what="past 4 GB")
+    wq.kv_paged_copy(cache, [[ids[0], pages - 3], [ids[2], 4]])
+    assert torch.equal(cache.pages[pages - 3], cache.pages[ids[0]])
+    assert torch.equal(cache.pages[4], cache.pages[ids[2]])
+    held = [cache.pages[int(p)].clone() for p in host.table[0, :3]]
+    table, used = wq.kv_paged_compact(cache, to_dev(host.lens))
+    assert int(used) == 5 and int(table.max()) == 4
+    for p, want in zip(table[0, :3].tolist(), held):
+        assert torch.equal(cache.pages[p], want)
+    cache.table = table
+    out = wq.kv_paged_attention(to_dev(q), cache, to_dev(host.lens))
+    check_attention(out, host, q, [0, 1, 2], what="compacted")
+
+
+def test_bench_paged_decode_step(capsys):
+    """The command's step at a small shape: every kernel timed, lengths within
+    the table, bytes counted."""
+    device()
+    sys.path.insert(0, ROOT)
+    import bench
+    note("bench paged decode step")
+    row = bench.run_kv_paged(SimpleNamespace(steps=130, warmup=2), shape=(3, 2, 4, 256), layers=2)
+    assert sorted(row["kernels"]) == ["kv_paged_append", "kv_paged_attention", "rope"]
+    assert row["roofline"]["bytes_per_step"] > 0 and row["config"]["tokens"] == 256
+    assert "kv_paged_decode" in capsys.readouterr().out

@@ -180,3 +180,10 @@ def test_rope_frequencies():
     for kw in (dict(rot=3), dict(rot=-2), dict(rot=4, kind="x"), dict(rot=4, base=0.0), dict(rot=4, factor=-1.0)):
         with pytest.raises(ValueError):
             wq.rope_frequencies(**kw, device="cpu")
+
+
+@pytest.mark.parametrize("kw", [dict(low=4.0, high=4.0), dict(low=5.0, high=4.0), dict(context=0)])
+def test_rope_frequencies_parts_refused(kw):
+    pytest.importorskip("torch")
+    with pytest.raises(ValueError):
+        wq.rope_frequencies(64, kind="parts", factor=2.0, device="cpu", **kw)
