@@ -586,7 +586,8 @@ def kv_paged_attention(q, cache: PagedKV, lens, seqs=None, window: int = 0, scal
     (rows may be strided parts of a packed row), q_heads a multiple of
     cache.heads -> out fp16 of the same shape, softmax(scale K q) V over the
     tokens lens says each slot holds.  seqs as in kv_paged_append; window > 0
-    keeps the last `window` tokens; scale defaults to 1 / sqrt(128).  The
+    keeps the last `window` tokens; scale defaults to 1 / sqrt(128); out does not
+    overlap q.  The
     workspace comes from torch or from `workspace` (kv_paged_workspace);
     use_workspace=False gives each sequence and KV head one workgroup."""
     import torch
