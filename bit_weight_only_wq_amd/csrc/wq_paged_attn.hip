@@ -46,8 +46,14 @@
 // The zero points enter as sum a_d z_d (a product with the zeros as B, once per
 // unit) and sum w_t z_t (in fp32, per lane).
 //
-// Ranges: q is scaled by a power of two per head so that |q| < 2, hence
-// |a| < 2 * 8736.  w is kept below 2^14 by the reference R of the running
+// Ranges: q is scaled by a power of two per head so that its largest channel is
+// 2^6 .. 2^7, and a block's key scales so that the largest is 2^7 .. 2^8 (as far as
+// a factor of 2^15 takes it), hence |a| < 2^15; both powers are taken out of the
+// score.  fp16 ends at 2^-24, so a channel's a keeps its 22 bits down to 2^-15 of
+// the product of those two (2^-11 in the odd channels), and what a smaller one
+// loses is below 2^-38 (2^-34) of it.  (Without the scales' power, keys of 2^-10
+// left relative errors of 2e-3 in the output, and of 2e-2 where they lie ten
+// deviations off zero.)  w is kept below 2^14 by the reference R of the running
 // exponent, R = max over units of (largest score + exponent of the largest
 // scale - 14), which also keeps the weights of tokens with small scales (and
 // those next to one that takes most of the weight but has small values) far
@@ -150,7 +156,11 @@ __device__ __forceinline__ h8_t unpack_k(uint32_t w) {
 __device__ __forceinline__ h8_t unpack_v(uint32_t w) {
     return as_h8(make_uint4((w << 4) & kHigh, w & kHigh, (w >> 4) & kHigh, (w >> 8) & kHigh));
 }
-constexpr float kKUnit = 0x1p24f, kVUnit = 0x1p20f;   // what scales the sums back
+// Exponents of a head's largest |q| and of a block's largest key scale, as
+// multiplied: their products stay below 2^15, and kQTop + 24 is the most that two
+// fp16 factors reach.
+constexpr int kQTop = 6, kSTop = 7;
+constexpr float kVUnit = 0x1p20f;         // what scales the values' sums back (the scores' 2^24 is in k_unit)
 // fp16 pairs: 2^-24, 2^-20, 1 / 16 and 16.
 constexpr uint32_t kEvenUnit = 0x00010001u, kOddUnit = 0x00100010u, kSixteenth = 0x2C002C00u, kSixteen = 0x4C004C00u;
 
@@ -429,8 +439,8 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
     };
-    // A new row, from its queries: turned through LDS to the slots' lanes, |q| < 2
-    // by a power of two that cn undoes.
+    // A new row, from its queries: turned through LDS to the slots' lanes, |q| <
+    // 2^(kQTop + 1) by a power of two that cn undoes.
     const auto start_row = [&](const Cursor& c, const uint4 (&piece)[NH]) {
         bad = false;
         in_blocks = true;
@@ -459,9 +469,9 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
         }
         turned();                             // (read before the weights come to the same place)
         const float top = column_max(half_bits_to_float(top2.x > top2.y ? top2.x : top2.y));
-        const int e = top > 0.0f ? __builtin_amdgcn_frexp_expf(top) - 1 : 0;   // top * 2^-e in [1, 2)
-        // (Within 2^-120 .. 2^80: no product with an infinity is 0 * inf.)
-        const float unit = __builtin_amdgcn_fmed3f(__builtin_amdgcn_ldexpf(__builtin_fabsf(A.scale), e), 0x1p-120f, 0x1p80f);
+        const int e = (top > 0.0f ? __builtin_amdgcn_frexp_expf(top) - 1 : 0) - kQTop;   // top * 2^-e in 2^kQTop * [1, 2)
+        // (Within 2^-90 .. 2^80: no product with an infinity is 0 * inf.)
+        const float unit = __builtin_amdgcn_fmed3f(__builtin_amdgcn_ldexpf(__builtin_fabsf(A.scale), e), 0x1p-90f, 0x1p80f);
 #pragma unroll
         for (int u = 0; u < NH; ++u) cn[u] = __shfl(unit, 4 * anew(g) + (kSplit ? 2 * u : u), 64);   // from the head's slot
         // 2^-e in two factors that fp16 holds, the second with scale's sign.
@@ -561,7 +571,22 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
         if (cu.block()) {
             bad |= cu.page < 0 || cu.page >= A.c.num_pages;
             // Headers to LDS: 16 bytes a lane in, the lane's 64 bytes of each out.
-            *reinterpret_cast<uint4*>(head_lds + 8 * anew(lane)) = H;
+            // K's scales (lanes 0 .. 15) go there times the power of two 2^up that
+            // brings the largest to 2^kSTop, as far as fp16 holds it.
+            us2_t s2 = us2_t{0, 0};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                s2 = __builtin_elementwise_max(s2, __builtin_bit_cast(us2_t, word(H, i) & 0x7FFF7FFFu));
+            const float s_top = row_max(half_bits_to_float(s2.x > s2.y ? s2.x : s2.y));
+            const int s_exp = (uniform(__builtin_bit_cast(int, s_top)) >> 23) - 127;
+            const int up = kSTop - s_exp < -14 ? -14 : (kSTop - s_exp > 15 ? 15 : kSTop - s_exp);   // (scales are below 2^16)
+            {
+                const int hl = anew(lane);
+                const uint32_t f = hl < 16 ? (uint32_t)(up + 15) * 0x04000400u : 0x3C003C00u;
+                *reinterpret_cast<uint4*>(head_lds + 8 * hl) =
+                    make_uint4(pk_mul(H.x, f), pk_mul(H.y, f), pk_mul(H.z, f), pk_mul(H.w, f));
+            }
+            const float k_unit = __builtin_bit_cast(float, (127 + 24 - up) << 23);   // 2^24 / 2^up
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
             __builtin_amdgcn_wave_barrier();
             const uint4* hd = reinterpret_cast<const uint4*>(head_lds) + 4 * g;   // + 16 per header array
@@ -627,13 +652,13 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
                 float top = sc[u][0];
 #pragma unroll
                 for (int r = 1; r < 8; ++r) top = __builtin_fmaxf(top, sc[u][r]);
-                cand[u] = __builtin_fmaf(top, cn[u] * kKUnit, above);
+                cand[u] = __builtin_fmaf(top, cn[u] * k_unit, above);
             }
             rebase(cand);
             uint4 low[NH];
 #pragma unroll
             for (int u = 0; u < NH; ++u) {
-                const float cc = cn[u] * kKUnit;
+                const float cc = cn[u] * k_unit;
                 float w[8];
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {
