@@ -54,10 +54,10 @@
 // loses is below 2^-38 (2^-34) of it.  (Without the scales' power, keys of 2^-10
 // left relative errors of 2e-3 in the output, and of 2e-2 where they lie ten
 // deviations off zero.)  w is kept below 2^14 by the reference R of the running
-// exponent, R = max over units of (largest score + exponent of the largest
-// scale - 14), which also keeps the weights of tokens with small scales (and
-// those next to one that takes most of the weight but has small values) far
-// above fp16's smallest numbers.
+// exponent, R = max over tokens of (score + exponent of its scale - 14): what is
+// rounded is the weight times the scale, and the largest of those products stays
+// near 2^13, whatever the scales beside it.  One below it by 2^-15 keeps its 22
+// bits, and a smaller one is off by 2^-38 of the largest.
 //
 // Measured, kernel and join together: 32 sequences of 4096 tokens with 32 heads
 // of their own (571 MB) 100 us, 5.7 TB/s; one of 131149 tokens with 64 query
@@ -162,6 +162,7 @@ __device__ __forceinline__ h8_t unpack_v(uint32_t w) {
 constexpr int kQTop = 6, kSTop = 7;
 constexpr float kVUnit = 0x1p20f;         // what scales the values' sums back (the scores' 2^24 is in k_unit)
 // fp16 pairs: 2^-24, 2^-20, 1 / 16 and 16.
+constexpr uint32_t kHalf1052 = 0x641C641Cu;   // 1024 (which an exponent field is taken to) + 28
 constexpr uint32_t kEvenUnit = 0x00010001u, kOddUnit = 0x00100010u, kSixteenth = 0x2C002C00u, kSixteen = 0x4C004C00u;
 
 __device__ __forceinline__ f4_t mfma(const h8_t& a, const h8_t& b, const f4_t& c) {
@@ -642,17 +643,21 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
             }
             const uint4 vs = reinterpret_cast<const uint4*>(head_lds)[32 + m];
             const uint4 vz = reinterpret_cast<const uint4*>(head_lds)[48 + m];
-            us2_t big = us2_t{0, 0};          // scales are positive: they order as their bits do
+            // The tokens' scales lie below 2^(x + 14), x the exponent field - 28 of each.
+            uint32_t x2[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) big = __builtin_elementwise_max(big, __builtin_bit_cast(us2_t, word(vs, i)));
-            const float above = (float)(__builtin_amdgcn_frexp_expf(half_bits_to_float(big.x > big.y ? big.x : big.y)) - 14);
+            for (int i = 0; i < 4; ++i)
+                x2[i] = as_u32(as_h2(((word(vs, i) >> 10) & 0x001F001Fu) | 0x64006400u) - as_h2(kHalf1052));
             float cand[NH];
 #pragma unroll
             for (int u = 0; u < NH; ++u) {
-                float top = sc[u][0];
+                const float cc = cn[u] * k_unit;
+                cand[u] = -__builtin_huge_valf();
 #pragma unroll
-                for (int r = 1; r < 8; ++r) top = __builtin_fmaxf(top, sc[u][r]);
-                cand[u] = __builtin_fmaf(top, cn[u] * k_unit, above);
+                for (int r = 0; r < 8; ++r) {
+                    const int e = r / 2 + 4 * (r & 1);
+                    cand[u] = __builtin_fmaxf(cand[u], __builtin_fmaf(sc[u][r], cc, (float)as_h2(x2[e >> 1])[e & 1]));
+                }
             }
             rebase(cand);
             uint4 low[NH];

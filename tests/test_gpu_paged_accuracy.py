@@ -76,3 +76,67 @@ def test_unlike_key_scales(group):
     for use_ws in (True, False):
         got = wq.kv_paged_attention(to_dev(q), cache, to_dev(host.lens), use_workspace=use_ws)
         assert head_errors(got, host.attend(q, [0])[0]).max() <= L2_REL
+
+
+# The bound below: a weight keeps 22 bits down to 2^-10 of the largest weight
+# times scale among the tokens it stands with, the values' sums 2^-16 of their
+# largest term; the result is rounded to fp16, by at most 2^-11 or, subnormal,
+# 2^-25.
+@pytest.mark.parametrize("group", GROUPS)
+@pytest.mark.parametrize("winner,loud", [(5, 2), (64, 71), (127, 120), (100, 30)])
+def test_small_values_beside_large(group, winner, loud):
+    """Two tokens share all of the weight, 1 to 3 to 1 to 1, and have values of 2^-14;
+    another of their block, far below them in score, has the largest values there
+    are."""
+    device()
+    rng = np.random.default_rng(winner)
+    heads, n = 2, G + 7
+    K = rng.standard_normal((n, heads, D)).astype(np.float16)
+    second = winner ^ 3
+    K[second] = K[winner]
+    V = rng.standard_normal((n, heads, D)) * 2.0 ** -14
+    V[loud] = rng.choice([-60000.0, 60000.0], (heads, D))
+    V = V.astype(np.float16)
+    q = np.repeat(8.0 * K[winner].astype(np.float64), group, 0)[None]
+    q = (q * (1 + rng.random(q.shape) / 4)).astype(np.float16)
+    K[second] *= np.float16(1 - 2.0 ** -7)
+    host, cache = held(K, V)
+    note(f"paged attention small values beside large group={group} {winner} {loud}")
+    ref, _ = host.attend(q, [0])
+    for h in range(heads):
+        k, v = host.cached(0, h)
+        for r in range(group):
+            s = k @ q[0, h * group + r].astype(np.float64) * D ** -0.5
+            assert s[winner] - np.delete(s, [winner, second]).max() > 40          # (60000 e^-40 is below 2^-41)
+        top = np.abs(v[winner]).max()
+        for use_ws in (True, False):
+            got = wq.kv_paged_attention(to_dev(q), cache, to_dev(host.lens), use_workspace=use_ws)
+            d = np.abs(got.cpu().numpy().astype(np.float64) - ref)[0, h * group:(h + 1) * group]
+            assert np.all(d <= 2.0 ** -16 * top + 2.0 ** -11 * np.abs(ref[0, h * group:(h + 1) * group]) + 2.0 ** -25)
+
+
+def test_sizes_apart_head_by_head():
+    """Keys of 2^-12, 1 and 2^5 and values of 2^-10, 1 and 2^9, queries that bring
+    each head's scores to a few units; in one head a token with values 2^-6 of the
+    others' takes more than 0.99 of the weight."""
+    device()
+    rng = np.random.default_rng(21)
+    n, heads, group = 700, 3, 4
+    K, V = rng.standard_normal((2, n, heads, D))
+    size = 2.0 ** np.array([0, -12, 5])[:, None]
+    K = (K * size).astype(np.float16)
+    V[5, 0] *= 2.0 ** -6
+    V = (V * 2.0 ** np.array([0, -10, 9])[:, None]).astype(np.float16)
+    q = rng.standard_normal((heads, group, D)) * 4 / size[..., None]
+    q[0, 0] = 1.5 * K[5, 0]
+    q[0, 1] = 1.75 * K[5, 0]
+    q = q.astype(np.float16).reshape(1, -1, D)
+    host, cache = held(K, V)
+    k, _ = host.cached(0, 0)
+    for r in range(2):
+        s = k @ q[0, r].astype(np.float64) * D ** -0.5
+        assert np.exp(s[5] - s.max()) / np.exp(s - s.max()).sum() > 0.99
+    note("paged attention sizes apart")
+    for use_ws in (True, False):
+        got = wq.kv_paged_attention(to_dev(q), cache, to_dev(host.lens), use_workspace=use_ws)
+        assert head_errors(got, host.attend(q, [0])[0]).max() <= L2_REL
