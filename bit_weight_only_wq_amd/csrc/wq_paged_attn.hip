@@ -44,7 +44,7 @@
 // for normal numbers), which a score bears (it is at most 1e-5 off) but a long
 // sum of positive weights does not.
 // The zero points enter as sum a_d z_d (a product with the zeros as B, once per
-// unit) and sum w_t z_t (in fp32, per lane).
+// unit) and sum w_t z_t (in fp32, per lane): any fp16 value, as a scale may be.
 //
 // Ranges: q is scaled by a power of two per head so that its largest channel is
 // 2^6 .. 2^7, and a block's key scales so that the largest is 2^7 .. 2^8 (as far as
@@ -161,9 +161,11 @@ __device__ __forceinline__ h8_t unpack_v(uint32_t w) {
 // fp16 factors reach.
 constexpr int kQTop = 6, kSTop = 7;
 constexpr float kVUnit = 0x1p20f;         // what scales the values' sums back (the scores' 2^24 is in k_unit)
-// fp16 pairs: 2^-24, 2^-20, 1 / 16 and 16.
-constexpr uint32_t kHalf1052 = 0x641C641Cu;   // 1024 (which an exponent field is taken to) + 28
-constexpr uint32_t kEvenUnit = 0x00010001u, kOddUnit = 0x00100010u, kSixteenth = 0x2C002C00u, kSixteen = 0x4C004C00u;
+constexpr float kZUnit = 0x1p-20f;        // of the zeros' sum, in the scores' sums
+// fp16 pairs: 1, 1 / 16 and 16, 1 / 16 beside 1, and 1024 (which an exponent field
+// is taken to) + 28.
+constexpr uint32_t kOnes = 0x3C003C00u, kSixteenth = 0x2C002C00u, kSixteen = 0x4C004C00u, kEvenSixteenth = 0x3C002C00u;
+constexpr uint32_t kHalf1052 = 0x641C641Cu;
 
 __device__ __forceinline__ f4_t mfma(const h8_t& a, const h8_t& b, const f4_t& c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
@@ -573,7 +575,8 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
             bad |= cu.page < 0 || cu.page >= A.c.num_pages;
             // Headers to LDS: 16 bytes a lane in, the lane's 64 bytes of each out.
             // K's scales (lanes 0 .. 15) go there times the power of two 2^up that
-            // brings the largest to 2^kSTop, as far as fp16 holds it.
+            // brings the largest to 2^kSTop, as far as fp16 holds it; K's zeros (lanes
+            // 16 .. 31) those of the even channels / 16, as the queries of the odd ones.
             us2_t s2 = us2_t{0, 0};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -583,7 +586,7 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
             const int up = kSTop - s_exp < -14 ? -14 : (kSTop - s_exp > 15 ? 15 : kSTop - s_exp);   // (scales are below 2^16)
             {
                 const int hl = anew(lane);
-                const uint32_t f = hl < 16 ? (uint32_t)(up + 15) * 0x04000400u : 0x3C003C00u;
+                const uint32_t f = hl < 16 ? (uint32_t)(up + 15) * 0x04000400u : (hl < 32 ? kEvenSixteenth : kOnes);
                 *reinterpret_cast<uint4*>(head_lds + 8 * hl) =
                     make_uint4(pk_mul(H.x, f), pk_mul(H.y, f), pk_mul(H.z, f), pk_mul(H.w, f));
             }
@@ -595,9 +598,7 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
             f4_t z4 = f4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const uint4 s = code_order(hd[j]), qj = *q_lds(j);
-                uint4 z = code_order(hd[16 + j]);       // in the codes' units (exact: at most 11 bits, above 2^-24)
-                z = make_uint4(pk_mul(z.x, kEvenUnit), pk_mul(z.y, kOddUnit), pk_mul(z.z, kEvenUnit), pk_mul(z.w, kOddUnit));
+                const uint4 s = code_order(hd[j]), z = code_order(hd[16 + j]), qj = *q_lds(j);
                 a0[j] = make_uint4(pk_mul(qj.x, s.x), pk_mul(qj.y, s.y), pk_mul(qj.z, s.z), pk_mul(qj.w, s.w));
                 a1[j] = make_uint4(pk_rest(qj.x, s.x, a0[j].x), pk_rest(qj.y, s.y, a0[j].y),
                                    pk_rest(qj.z, s.z, a0[j].z), pk_rest(qj.w, s.w, a0[j].w));
@@ -607,9 +608,10 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
                 z4 = mfma(as_h8(a0[j]), as_h8(z), z4);
                 if (!kSplit) z4 = mfma(as_h8(a1[j]), as_h8(z), z4);
             }
+            z4 *= -kZUnit;
             f4_t S[8];
 #pragma unroll
-            for (int r = 0; r < 8; ++r) S[r] = -z4;
+            for (int r = 0; r < 8; ++r) S[r] = z4;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll

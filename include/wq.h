@@ -501,7 +501,8 @@ wq_status wq_kv_paged_append(const void* k, const void* v, int64_t tokens, int64
  * Decode attention of one new token per sequence over the paged cache:
  *     out[i, g] = softmax(scale * K_h q[i, g]) V_h,  h = g / (q_heads / heads)
  * over the tokens that entry i's slot holds (the new one appended before),
- * dequantized as (c - z) * s; window > 0 keeps the last `window` tokens only.
+ * dequantized as (c - z) * s with whatever finite fp16 zeros and scales the
+ * records hold; window > 0 keeps the last `window` tokens only.
  * q_heads is a multiple of heads.  No token to see (an empty or padded entry)
  * gives zeros; lens are clamped to [0, max_pages * 128 + 127]; a table entry
  * outside [0, num_pages) among the blocks that are read gives NaN in that

@@ -140,3 +140,38 @@ def test_sizes_apart_head_by_head():
     for use_ws in (True, False):
         got = wq.kv_paged_attention(to_dev(q), cache, to_dev(host.lens), use_workspace=use_ws)
         assert head_errors(got, host.attend(q, [0])[0]).max() <= L2_REL
+
+
+@pytest.mark.parametrize("group", GROUPS)
+@pytest.mark.parametrize("window", [0, 200])
+def test_any_headers(group, window):
+    """Headers that the append does not write: zeros with fractions, scales of
+    either sign.  A value is (c - z) s all the same."""
+    device()
+    rng = np.random.default_rng(7 * group + window)
+    heads, blocks = 2, 5
+    codes = rng.integers(0, 256, (blocks, heads, 16384)).astype(np.uint8)
+    sign = lambda: rng.choice([-1.0, 1.0], (blocks, heads, 1, 128))  # noqa: E731
+    head = np.concatenate([sign() * rng.uniform(0.1, 0.4, (blocks, heads, 1, 128)),
+                           rng.uniform(4, 11, (blocks, heads, 1, 128)),
+                           sign() * rng.uniform(0.01, 0.4, (blocks, heads, 1, 128)),
+                           rng.uniform(4, 11, (blocks, heads, 1, 128))], 2).astype(np.float16)
+    rec = np.concatenate([codes, head.reshape(blocks, heads, 512).view(np.uint8)], 2)
+    assert rec.shape[2] == REC
+    cache = wq.PagedKV(heads, blocks, 1, blocks)
+    cache.pages.copy_(to_dev(rec))
+    cache.table.copy_(to_dev(np.arange(blocks, dtype=np.int32)[None]))
+    q = rng.standard_normal((1, heads * group, D)).astype(np.float16)
+    ref = np.zeros((1, heads * group, D))
+    for h in range(heads):
+        K, V = [np.concatenate(x) for x in zip(*[okv.dequantize_block(dict(
+            kcodes=rec[b, h, :8192].reshape(G, 64), vcodes=rec[b, h, 8192:16384].reshape(D, 64), ks=head[b, h, 0],
+            kz=head[b, h, 1], vs=head[b, h, 2], vz=head[b, h, 3])) for b in range(blocks)])]
+        first = max(0, len(K) - window) if window else 0
+        for r in range(h * group, (h + 1) * group):
+            ref[0, r] = okv.attend(q[0, r], K[first:], V[first:], D ** -0.5)
+    lens = to_dev(np.array([blocks * G], np.int32))
+    note(f"paged attention any headers group={group} window={window}")
+    for use_ws in (True, False):
+        got = wq.kv_paged_attention(to_dev(q), cache, lens, window=window, use_workspace=use_ws)
+        assert head_errors(got, ref).max() <= L2_REL
