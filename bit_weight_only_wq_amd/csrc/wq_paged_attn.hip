@@ -56,8 +56,9 @@
 // deviations off zero.)  w is kept below 2^14 by the reference R of the running
 // exponent, R = max over tokens of (score + exponent of its scale - 14): what is
 // rounded is the weight times the scale, and the largest of those products stays
-// near 2^13, whatever the scales beside it.  One below it by 2^-15 keeps its 22
-// bits, and a smaller one is off by 2^-38 of the largest.
+// near 2^13, whatever the scales beside it (2^13 / 2^x where that scale is 2^-x of
+// 1/4).  One below it by 2^-15 keeps its 22 bits, and a smaller one is off by 2^-38
+// of the largest.
 //
 // Measured, kernel and join together: 32 sequences of 4096 tokens with 32 heads
 // of their own (571 MB) 100 us, 5.7 TB/s; one of 131149 tokens with 64 query
@@ -127,6 +128,12 @@ __device__ __forceinline__ Span span_of(int len, int64_t window) {
 __device__ __forceinline__ int anew(int v) {
     asm volatile("" : "+v"(v));
     return v;
+}
+
+// a b, rounded: what follows does not take the product into an fma.
+__device__ __forceinline__ float rounded_product(float a, float b) {
+#pragma clang fp contract(off)
+    return a * b;
 }
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -543,12 +550,18 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
         const auto nbuf = buffer(nx, more);
 
         // New reference for the running exponent, and what is held with the old one.
+        // Past 2^24 a score and its reference are rounded by more than they are
+        // apart (at most 15, see x2).  So the reference goes up by two steps of fp32,
+        // but not by 16: then, at any size, no weight leaves fp16 at the top, and the
+        // largest does not vanish.  (A step of 16: -15 .. 0 is rounded to -16 or 0, and
+        // 16 is added; of 32 and more: both are rounded away.)
         const auto rebase = [&](const float (&cand)[NH]) {
             float alpha[NH];
             bool grows = false;
 #pragma unroll
             for (int u = 0; u < NH; ++u) {
-                const float r = __builtin_fmaxf(R[u], row_max(cand[u]));
+                const float c = row_max(cand[u]);
+                const float r = __builtin_fmaxf(R[u], c + __builtin_fminf(__builtin_fabsf(c) * 0x1p-23f, 15.9f));
                 grows |= r > R[u];
                 alpha[u] = R[u] - r;
                 R[u] = r;
@@ -622,12 +635,14 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
                 }
             load_k(nbuf, K, H);
 
-            // Scores of the lane's tokens 8 m + place(r) for its heads.
-            float sc[NH][8];
+            // Scores of the lane's tokens 8 m + place(r) for its heads, times cc in log2.
+            float sc[NH][8], cc[NH];
 #pragma unroll
-            for (int u = 0; u < NH; ++u)
+            for (int u = 0; u < NH; ++u) {
+                cc[u] = cn[u] * k_unit;
 #pragma unroll
                 for (int r = 0; r < 8; ++r) sc[u][r] = kSplit ? S[r][(2 * u) & 3] + S[r][(2 * u + 1) & 3] : S[r][u];
+            }
             // Tokens left of the window do not count, whatever they hold.
             const int skip = cu.s.left - (cu.s.b0 + cu.unit) * kG;
             if (skip > 0) {
@@ -645,32 +660,50 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
             }
             const uint4 vs = reinterpret_cast<const uint4*>(head_lds)[32 + m];
             const uint4 vz = reinterpret_cast<const uint4*>(head_lds)[48 + m];
-            // The tokens' scales lie below 2^(x + 14), x the exponent field - 28 of each.
+            // The tokens' scales lie below 2^(x + 14), x the exponent field - 28 of each,
+            // but no less than -15.
             uint32_t x2[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                x2[i] = as_u32(as_h2(((word(vs, i) >> 10) & 0x001F001Fu) | 0x64006400u) - as_h2(kHalf1052));
+            for (int i = 0; i < 4; ++i) {
+                const us2_t field = __builtin_elementwise_max(__builtin_bit_cast(us2_t, (word(vs, i) >> 10) & 0x001F001Fu),
+                                                              us2_t{13, 13});
+                x2[i] = as_u32(as_h2(__builtin_bit_cast(uint32_t, field) | 0x64006400u) - as_h2(kHalf1052));
+            }
             float cand[NH];
+            const auto candidates = [&]() {
+                float far = 0.0f;
 #pragma unroll
-            for (int u = 0; u < NH; ++u) {
-                const float cc = cn[u] * k_unit;
-                cand[u] = -__builtin_huge_valf();
+                for (int u = 0; u < NH; ++u) {
+                    cand[u] = -__builtin_huge_valf();
 #pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    const int e = r / 2 + 4 * (r & 1);
-                    cand[u] = __builtin_fmaxf(cand[u], __builtin_fmaf(sc[u][r], cc, (float)as_h2(x2[e >> 1])[e & 1]));
+                    for (int r = 0; r < 8; ++r) {
+                        const int e = r / 2 + 4 * (r & 1);
+                        cand[u] = __builtin_fmaxf(cand[u], __builtin_fmaf(sc[u][r], cc[u], (float)as_h2(x2[e >> 1])[e & 1]));
+                    }
+                    far = __builtin_fmaxf(far, __builtin_fabsf(cand[u]));
                 }
+                return far;
+            };
+            // Far scores are rounded first: then the exponents below take one number
+            // from itself, and not from another that is rounded by more than 1.
+            if (__builtin_amdgcn_ballot_w64(candidates() >= 0x1p20f) != 0) {
+#pragma unroll
+                for (int u = 0; u < NH; ++u) {
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) sc[u][r] = rounded_product(sc[u][r], cc[u]);
+                    cc[u] = 1.0f;
+                }
+                candidates();
             }
             rebase(cand);
             uint4 low[NH];
 #pragma unroll
             for (int u = 0; u < NH; ++u) {
-                const float cc = cn[u] * k_unit;
                 float w[8];
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {
                     const int e = r / 2 + 4 * (r & 1);
-                    const float p = exp2_hw(__builtin_fmaf(sc[u][r], cc, -R[u]));
+                    const float p = exp2_hw(__builtin_fmaf(sc[u][r], cc[u], -R[u]));
                     L[u] += p;
                     w[r] = __builtin_fmaf(p, (float)as_h2(word(vs, e >> 1))[e & 1], zero);   // (one v_fma_mix)
                     cz[u] = __builtin_fmaf(w[r], (float)as_h2(word(vz, e >> 1))[e & 1], cz[u]);
@@ -742,9 +775,9 @@ __global__ __launch_bounds__(kThreads, 2) void paged_attn_kernel(const AttnArgs 
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const int t = t0 + 16 * r + mw;
-                    sc[u][r] = t >= begin && t < end ? S[r][kSplit ? (2 * u) & 3 : u] * cn[u] : -__builtin_huge_valf();
+                    sc[u][r] = t >= begin && t < end ? rounded_product(S[r][kSplit ? (2 * u) & 3 : u], cn[u]) : -__builtin_huge_valf();
                 }
-                cand[u] = __builtin_fmaxf(sc[u][0], sc[u][1]) + (float)(1 - 14);
+                cand[u] = __builtin_fmaxf(sc[u][0], sc[u][1]) + (float)(1 - 14);   // (as a scale of 1)
             }
             rebase(cand);
             uint32_t low[NH];

@@ -175,3 +175,34 @@ def test_any_headers(group, window):
     for use_ws in (True, False):
         got = wq.kv_paged_attention(to_dev(q), cache, lens, window=window, use_workspace=use_ws)
         assert head_errors(got, ref).max() <= L2_REL
+
+
+@pytest.mark.parametrize("vsize", [2.0 ** -8, 1.0, 2.0 ** 8])
+@pytest.mark.parametrize("group", GROUPS)
+def test_far_scores(group, vsize):
+    """Scores from 2^20 to 2^34 units of the exponent, of either sign: past 2^24
+    neighbouring fp32 numbers are whole powers of two apart.  One token wins by
+    far, in a block or in the window; its values come back.  (Its weight is rounded to
+    2^-14 at worst: 2^-25 of what is left of 2^13 after two steps of 16, 2^-11.)"""
+    device()
+    rng = np.random.default_rng(group)
+    heads, n = 2, 2 * G + 50
+    u = rng.choice([-1.0, 1.0], (heads, D))
+    V = (rng.standard_normal((n, heads, D)) * vsize).astype(np.float16)
+    for best, least in ((77, 200), (2 * G + 33, 2 * G + 5), (200, 2 * G + 49)):
+        level = rng.integers(1, 15, n).astype(np.float64)
+        level[best], level[least] = 15.0, 0.0
+        for half in range(18, 32):                        # the largest |K| and |q| are 2^(half / 2)
+            size = min(2.0 ** (half / 2), 60000.0)
+            K = ((level[:, None, None] / 15 - 0.5) * u * size).astype(np.float16)
+            q = np.repeat(u, group, 0) * size
+            q[group // 2:group] *= -1.0                   # these point at `least`
+            q = q[None].astype(np.float16)
+            host, cache = held(K, V)
+            note(f"paged attention far scores group={group} {best} 2^{half / 2}")
+            with np.errstate(over="ignore"):              # (attend's own bound is not used)
+                ref, _ = host.attend(q, [0])
+            bound = 2.0 ** -11 * np.abs(ref) + 2.0 ** -13 * np.abs(V).max() + 2.0 ** -25
+            for use_ws in (True, False):
+                got = wq.kv_paged_attention(to_dev(q), cache, to_dev(host.lens), use_workspace=use_ws)
+                assert np.all(np.abs(got.cpu().numpy().astype(np.float64) - ref) <= bound), half
