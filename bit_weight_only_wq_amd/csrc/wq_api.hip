@@ -751,6 +751,9 @@ wq_status wq_kv_paged_attention(const void* q, int64_t q_stride, int64_t q_heads
     if (!aligned(q, 16) || q_stride % 8 != 0 || !aligned(out, 8) || out_stride % 4 != 0)
         return fail(WQ_ERR_MISALIGNED, "wq_kv_paged_attention: q and its stride need 16-byte, out and its stride 8-byte "
                     "alignment");
+    if (need == 0 && !wq::paged_attention_rows_fit(a, q_heads, count))
+        return fail(WQ_ERR_UNSUPPORTED, "wq_kv_paged_attention: too many rows without a workspace (count=%lld "
+                    "q_heads=%lld)", count, q_heads);
     wq::Scratch ws;
     ws.ptr = need > 0 ? workspace : nullptr;
     return check_hip(wq::launch_paged_attention(q, q_stride, q_heads, a, lens, seqs, count, window, scale, out, out_stride,

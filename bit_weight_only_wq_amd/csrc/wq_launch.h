@@ -192,6 +192,9 @@ hipError_t launch_paged_attention(const void* q, int64_t q_stride, int64_t q_hea
                                   const int32_t* lens, const int32_t* seqs, int64_t count, int64_t window,
                                   float scale, void* out, int64_t out_stride, int num_cus, const Scratch& ws,
                                   hipStream_t stream);
+// Whether one workgroup per row (entry, KV head and chunk of its query heads) fits
+// a grid: HIP takes fewer than 2^32 threads in a dimension.
+bool paged_attention_rows_fit(const PagedArgs& c, int64_t q_heads, int64_t count);
 hipError_t launch_paged_copy(const PagedArgs& c, const int32_t* pairs, int64_t count, hipStream_t stream);
 hipError_t launch_paged_fork(const PagedArgs& c, int32_t* lens, const int32_t* pairs, int64_t count,
                              hipStream_t stream);

@@ -1042,6 +1042,11 @@ __global__ __launch_bounds__(kJoin) void paged_join_kernel(const AttnArgs A) {
 
 }  // namespace
 
+bool paged_attention_rows_fit(const PagedArgs& c, int64_t q_heads, int64_t count) {
+    const int64_t chunks = (q_heads / c.heads + kMaxRow - 1) / kMaxRow;
+    return count * c.heads * chunks * kThreads < ((int64_t)1 << 32);
+}
+
 hipError_t launch_paged_attention(const void* q, int64_t q_stride, int64_t q_heads, const PagedArgs& c,
                                   const int32_t* lens, const int32_t* seqs, int64_t count, int64_t window,
                                   float scale, void* out, int64_t out_stride, int num_cus, const Scratch& ws,

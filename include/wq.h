@@ -519,7 +519,8 @@ wq_status wq_kv_paged_append(const void* k, const void* v, int64_t tokens, int64
  * workspace, or for a few short sequences, one workgroup takes each sequence
  * and KV head (and each 16 of its query heads).
  * count <= 65535, count * q_heads < 2^24 and count * q_heads * (max_pages + 4)
- * < 2^31 (WQ_ERR_UNSUPPORTED otherwise).
+ * < 2^31; without a workspace those workgroups, count * heads * ceil(q_heads /
+ * heads / 16), must be below 2^23 (WQ_ERR_UNSUPPORTED otherwise).
  */
 wq_status wq_kv_paged_attention(const void* q, int64_t q_stride, int64_t q_heads,
                                 const wq_kv_paged* cache, const int32_t* lens, const int32_t* seqs,

@@ -109,3 +109,26 @@ def test_bench_paged_decode_step(capsys):
     assert sorted(row["kernels"]) == ["kv_paged_append", "kv_paged_attention", "rope"]
     assert row["roofline"]["bytes_per_step"] > 0 and row["config"]["tokens"] == 256
     assert "kv_paged_decode" in capsys.readouterr().out
+
+
+def test_attention_most_rows_without_a_workspace():
+    """65535 entries of 128 heads, 128 rows below what a grid takes: three hold
+    tokens, the others are padding and give zeros."""
+    dev = device()
+    heads = 128
+    rng = np.random.default_rng(6)
+    host = Host(heads, 2, 3, 1)
+    cache = gpu_cache(wq, host)
+    append(wq, cache, host, [(s, *draw_tokens(rng, n, heads)) for s, n in enumerate((3, 130, 40))])
+    seqs = np.full(65535, -1, np.int32)
+    at = [0, 40000, 65534]
+    seqs[at] = [2, 0, 1]
+    q = rng.standard_normal((3, heads, D)).astype(np.float16)
+    big = torch.zeros((65535, heads, D), dtype=torch.float16, device=dev)
+    big[at] = to_dev(q)
+    out = torch.full_like(big, 3.0)
+    note("paged attention with 8388480 rows")
+    wq.kv_paged_attention(big, cache, to_dev(host.lens), seqs=to_dev(seqs), out=out, use_workspace=False)
+    check_attention(out[at], host, q, [2, 0, 1], what="most rows")
+    out[at] = 0
+    assert not out.any()

@@ -187,3 +187,15 @@ def test_rope_frequencies_parts_refused(kw):
     pytest.importorskip("torch")
     with pytest.raises(ValueError):
         wq.rope_frequencies(64, kind="parts", factor=2.0, device="cpu", **kw)
+
+
+@pytest.mark.parametrize("heads,group,n", [(129, 1, 65535), (8192, 1, 1024), (4096, 1, 2048), (32767, 1, 512)])
+def test_attention_rows_past_a_grid(heads, group, n):
+    """Without a workspace a row is a workgroup of 512 threads, and a grid takes
+    fewer than 2^32 threads: refused before any launch."""
+    c = ctypes.byref(paged(heads=heads, slots=65535, max_pages=1))
+    qh, need = heads * group, ctypes.c_size_t(0)
+    assert n * heads * -(-group // 16) >= 1 << 23 and n * qh < 1 << 24
+    assert attend(c=c, n=n, qh=qh, qs=qh * 128, os_=qh * 128) == UNSUP
+    assert b"workspace" in wq.load().wq_last_error()
+    assert wq.load().wq_kv_paged_workspace_size(c, n, qh, ctypes.byref(need)) == OK
