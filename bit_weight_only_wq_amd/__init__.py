@@ -586,10 +586,10 @@ def kv_paged_attention(q, cache: PagedKV, lens, seqs=None, window: int = 0, scal
     (rows may be strided parts of a packed row), q_heads a multiple of
     cache.heads -> out fp16 of the same shape, softmax(scale K q) V over the
     tokens lens says each slot holds.  seqs as in kv_paged_append; window > 0
-    keeps the last `window` tokens; scale defaults to 1 / sqrt(128); out does not
-    overlap q.  The
-    workspace comes from torch or from `workspace` (kv_paged_workspace);
-    use_workspace=False gives each sequence and KV head one workgroup."""
+    keeps the last `window` tokens; scale defaults to 1 / sqrt(128); out must not
+    overlap q (it may lie beside it in one packed row).  The workspace comes
+    from torch or from `workspace` (kv_paged_workspace); use_workspace=False
+    gives each sequence and KV head one workgroup."""
     import torch
     dev = cache.device
     qs = _heads_rows(q, None, "q", dev)
@@ -602,6 +602,8 @@ def kv_paged_attention(q, cache: PagedKV, lens, seqs=None, window: int = 0, scal
         os_ = _heads_rows(out, Hq, "out", dev)
         if out.shape[0] != S:
             raise ValueError(f"out must have q's shape {tuple(q.shape)}, got {tuple(out.shape)}")
+        if out.numel() and _rows_meet(q, out):
+            raise ValueError("out overlaps q")
     if workspace is None and use_workspace:
         workspace = kv_paged_workspace(cache, S, Hq)
     wp, wn = _given(workspace, dev) if workspace is not None and use_workspace else (None, 0)

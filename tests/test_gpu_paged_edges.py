@@ -11,7 +11,7 @@ import pytest
 from conftest import ROOT
 from gpu_util import device, note, to_dev
 from paged_util import D, G, Host, append, draw_tokens, gpu_cache
-from test_gpu_paged import check_attention, i32
+from test_gpu_paged import check_attention, filled, i32
 
 import bit_weight_only_wq_amd as wq
 
@@ -132,3 +132,23 @@ def test_attention_most_rows_without_a_workspace():
     check_attention(out[at], host, q, [2, 0, 1], what="most rows")
     out[at] = 0
     assert not out.any()
+
+
+def test_attention_out_over_q_refused():
+    """q itself, a shifted view of its packed row, rows one entry on: refused.
+    Beside q in the row: taken."""
+    dev = device()
+    host, cache, rng = filled(2, [77, 300, 128], 31)
+    q = rng.standard_normal((3, 4, D)).astype(np.float16)
+    row = torch.zeros((4, 12, D), dtype=torch.float16, device=dev)
+    row[:3, :4] = to_dev(q)
+    args = dict(cache=cache, lens=to_dev(host.lens), seqs=i32([1, 2, 3]))
+    for out in (row[:3, :4], row[:3, 1:5], row[:3, 3:7], row[1:, :4], row.view(-1, 4, D)[1:4]):
+        before = row.clone()
+        with pytest.raises(ValueError):
+            wq.kv_paged_attention(row[:3, :4], out=out, **args)
+        assert torch.equal(row, before)
+    note("paged attention beside its q")
+    for out in (row[:3, 4:8], row[:3, 8:]):
+        got = wq.kv_paged_attention(row[:3, :4], out=out, **args)
+        check_attention(got, host, q, [1, 2, 3], what="beside q")
