@@ -11,6 +11,8 @@ library is not built, the calls raise.
 
 from __future__ import annotations
 
+from operator import attrgetter
+
 from . import roofline  # noqa: F401  (pure arithmetic, no GPU)
 from ._lib import (WQ_PATH_AUTO, WQ_PATH_GEMV, WQ_PATH_MFMA, WQError,  # noqa: F401
                    LIB_PATH, check, load)
@@ -457,7 +459,9 @@ class PagedKV:
     """Caller-owned buffers of one layer's paged int4 KV cache, as torch tensors
     on one GPU; layout as wq_kv_paged in wq.h.  Either new, zeroed buffers of the
     given sizes, or existing ones: pages u8 [num_pages, heads, 17408], windows
-    fp16 [slots, heads, 2, 128, 128], table int32 [slots, max_pages].
+    fp16 [slots, heads, 2, 128, 128], table int32 [slots, max_pages].  The three
+    may be set anew (pages of any number, windows and table of the same slots);
+    the sizes follow them and cannot be set.
 
         cache = PagedKV(heads=8, num_pages=4096, slots=64, max_pages=256)
         cache.table[slot, block] = page        # which page a block will get
@@ -479,16 +483,44 @@ class PagedKV:
         if table is None:
             table = torch.full((windows.shape[0], max_pages), -1, dtype=torch.int32, device=pages.device)
         _gpu(pages, torch.uint8, "pages")
+        self._pages = self._windows = self._table = None
+        self._device = pages.device
+        self.pages = pages
+        self.windows = windows
+        self.table = table
+
+    @property
+    def pages(self):
+        return self._pages
+
+    @pages.setter
+    def pages(self, pages):
+        import torch
+        _gpu(pages, torch.uint8, "pages", self._device)
         if pages.dim() != 3 or pages.shape[2] != self.RECORD or not pages.is_contiguous():
             raise ValueError(f"pages must be contiguous [num_pages, heads, {self.RECORD}], got {tuple(pages.shape)}")
-        self.pages, self.device = pages, pages.device
-        self.num_pages, self.heads = pages.shape[0], pages.shape[1]
-        _gpu(windows, torch.float16, "windows", self.device)
-        if tuple(windows.shape[1:]) != (self.heads, 2, self.G, self.D) or not windows.is_contiguous():
+        if self._windows is not None and pages.shape[1] != self.heads:
+            raise ValueError(f"pages must be of {self.heads} heads, got {pages.shape[1]}")
+        self._pages = pages
+        self._num_pages, self._heads = pages.shape[:2]
+        self._describe()
+
+    @property
+    def windows(self):
+        return self._windows
+
+    @windows.setter
+    def windows(self, windows):
+        import torch
+        _gpu(windows, torch.float16, "windows", self._device)
+        if (windows.dim() != 5 or tuple(windows.shape[1:]) != (self.heads, 2, self.G, self.D)
+                or not windows.is_contiguous()):
             raise ValueError(f"windows must be contiguous [slots, {self.heads}, 2, {self.G}, {self.D}], "
                              f"got {tuple(windows.shape)}")
-        self.windows, self.slots = windows, windows.shape[0]
-        self.table = table
+        if self._table is not None and windows.shape[0] != self.slots:
+            raise ValueError(f"windows must be of {self.slots} slots, got {windows.shape[0]}")
+        self._windows, self._slots = windows, windows.shape[0]
+        self._describe()
 
     @property
     def table(self):
@@ -496,14 +528,26 @@ class PagedKV:
 
     @table.setter
     def table(self, table):
-        import ctypes
         import torch
-        from ._lib import KvPaged
-        _gpu(table, torch.int32, "table", self.device)
+        _gpu(table, torch.int32, "table", self._device)
         if table.dim() != 2 or table.shape[0] != self.slots or not table.is_contiguous():
             raise ValueError(f"table must be contiguous [{self.slots}, max_pages], got {tuple(table.shape)}")
-        self._table, self.max_pages = table, table.shape[1]
-        self._desc = KvPaged(self.pages.data_ptr(), self.windows.data_ptr(), table.data_ptr(), self.heads,
+        self._table, self._max_pages = table, table.shape[1]
+        self._describe()
+
+    # (attrgetter: a call of one token asks for these often enough to count)
+    device = property(attrgetter("_device"))
+    num_pages = property(attrgetter("_num_pages"))
+    heads = property(attrgetter("_heads"))
+    slots = property(attrgetter("_slots"))
+    max_pages = property(attrgetter("_max_pages"))
+
+    def _describe(self):
+        import ctypes
+        from ._lib import KvPaged
+        if self._table is None:            # (still in __init__)
+            return
+        self._desc = KvPaged(self._pages.data_ptr(), self._windows.data_ptr(), self._table.data_ptr(), self.heads,
                              self.num_pages, self.slots, self.max_pages)
         self._ref = ctypes.byref(self._desc)
 

@@ -152,3 +152,43 @@ def test_attention_out_over_q_refused():
     for out in (row[:3, 4:8], row[:3, 8:]):
         got = wq.kv_paged_attention(row[:3, :4], out=out, **args)
         check_attention(got, host, q, [1, 2, 3], what="beside q")
+
+
+def test_replaced_buffers_are_the_ones_used():
+    """pages, windows and table set anew (a packed pool cut to what is in use):
+    every call follows; what does not fit, and the sizes themselves, cannot be
+    set."""
+    dev = device()
+    host, cache, rng = filled(2, [300, 700, 40], 33, max_pages=7, extra_pages=20)
+    q = rng.standard_normal((3, 4, D)).astype(np.float16)
+    slots, lens = [1, 2, 3], to_dev(host.lens)
+    old = cache.pages
+    note("paged cache with its buffers replaced")
+    table, used = wq.kv_paged_compact(cache, lens)
+    n = int(used.item())
+    cache.table = table
+    cache.pages = cache.pages[:n + 2].clone()
+    cache.windows = cache.windows.clone()
+    old.fill_(0x5A)                                   # nobody's any more
+    assert (cache.num_pages, cache.descriptor().num_pages) == (n + 2, n + 2)
+    check_attention(wq.kv_paged_attention(to_dev(q), cache, lens, seqs=i32(slots)), host, q, slots, what="cut")
+    host.table, host.free = table.cpu().numpy(), [n + 1, n]
+    append(wq, cache, host, [(1, *draw_tokens(rng, 100, 2)), (3, *draw_tokens(rng, 90, 2))])
+    host.check_buffers(cache, "cut")
+    assert torch.all(old == 0x5A)
+    cache.table[1, 0] = n + 2                         # an id of the old pool only
+    lens = to_dev(host.lens)
+    out = wq.kv_paged_attention(to_dev(q), cache, lens, seqs=i32(slots))
+    assert torch.isnan(out[0]).all()
+    check_attention(out[1:], host, q[1:], slots[1:], what="beside a page past the pool")
+    held = cache.pages, cache.windows, cache.table
+    for name, bad in [("pages", cache.pages[:, :1].contiguous()), ("pages", cache.pages[:, :, :100]),
+                      ("pages", cache.pages.cpu()), ("pages", cache.pages.view(torch.int8)),
+                      ("windows", cache.windows[:1]), ("windows", cache.windows[:, :1].contiguous()),
+                      ("windows", cache.windows.float()), ("table", cache.table[:2]), ("table", cache.table.long())]:
+        with pytest.raises(ValueError):
+            setattr(cache, name, bad)
+    for name in ("num_pages", "heads", "slots", "max_pages", "device"):
+        with pytest.raises(AttributeError):
+            setattr(cache, name, getattr(cache, name))
+    assert all(a is b for a, b in zip(held, (cache.pages, cache.windows, cache.table)))
