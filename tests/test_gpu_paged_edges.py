@@ -192,3 +192,33 @@ def test_replaced_buffers_are_the_ones_used():
         with pytest.raises(AttributeError):
             setattr(cache, name, getattr(cache, name))
     assert all(a is b for a, b in zip(held, (cache.pages, cache.windows, cache.table)))
+
+
+def test_compact_at_the_border_of_a_range():
+    """The plan marks 131072 pages at a time: pages in use and free on both sides
+    of that border, the first and the last of either range, fewer and more of
+    them in use than a range holds."""
+    dev = device()
+    R = 131072
+    P = R + 200                                       # 2.3 GB of one head
+    cache = wq.PagedKV(1, P, 2, R + 100)
+    rng = np.random.default_rng(3)
+    for rows in ([[R - 1, R, 0, P - 1], [R + 1, R - 2, 5]], [[R], [R - 1]],
+                 [np.delete(np.arange(R + 90), [3, R - 1, R, R + 7])[rng.permutation(R + 86)], [P - 1, R + 150]]):
+        lens, table = np.zeros(2, np.int32), np.full((2, R + 100), -1, np.int32)
+        for s, r in enumerate(rows):
+            table[s, :len(r)], lens[s] = r, len(r) * G
+        held = np.unique(np.concatenate([np.asarray(r) for r in rows]))
+        cache.pages.view(torch.int32)[:, 0, 17] = torch.arange(P, dtype=torch.int32, device=dev)
+        cache.table.copy_(to_dev(table))
+        note(f"paged compact of {len(held)} pages about {R}")
+        new, used = wq.kv_paged_compact(cache, to_dev(lens))
+        n = int(used.item())
+        assert n == len(held)
+        new, got = new.cpu().numpy(), cache.pages.view(torch.int32)[:, 0, 17].cpu().numpy()
+        for s, r in enumerate(rows):
+            ids = new[s, :len(r)]
+            assert np.all((ids >= 0) & (ids < n)) and np.array_equal(got[ids], r), s
+            assert np.all(new[s, len(r):] == -1)
+            assert np.array_equal(ids[np.asarray(r) < n], np.asarray(r)[np.asarray(r) < n])      # these stay
+        assert len(np.unique(np.concatenate([new[s, :len(r)] for s, r in enumerate(rows)]))) == n
