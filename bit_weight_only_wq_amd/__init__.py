@@ -11,6 +11,7 @@ library is not built, the calls raise.
 
 from __future__ import annotations
 
+import math
 from operator import attrgetter
 
 from . import roofline  # noqa: F401  (pure arithmetic, no GPU)
@@ -378,7 +379,9 @@ def _line(t, dtype, n, name, device):
 
 def _rows_meet(a, b):
     """Whether [T, H, D] tensors a and b (last stride 1) share memory, told from
-    their extents: rows of one token stride that lie side by side are apart."""
+    their extents: rows of one token stride that lie side by side are apart, and
+    so are heads that lie side by side at every multiple of all strides' common
+    divisor."""
     size = a.element_size()
     extent = lambda t: sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1  # noqa: E731
     ea, eb = extent(a), extent(b)
@@ -388,8 +391,10 @@ def _rows_meet(a, b):
     step = a.stride(0)
     if step == b.stride(0) and step > 0:
         ra, rb = (1 + (t.shape[1] - 1) * t.stride(1) + t.shape[2] - 1 for t in (a, b))
-        return not (ra <= d % step <= step - rb)
-    return True
+        if ra <= d % step <= step - rb:
+            return False
+    step = math.gcd(*(s for t in (a, b) for n, s in zip(t.shape[:2], t.stride()) if n > 1))
+    return not (step > 0 and a.shape[2] <= d % step <= step - b.shape[2])
 
 
 def rope_frequencies(rot: int, base: float = 10000.0, kind: str = "none", factor: float = 1.0, context: int = 4096,
@@ -403,7 +408,6 @@ def rope_frequencies(rot: int, base: float = 10000.0, kind: str = "none", factor
       "parts"   pairs that turn less than `low` times within `context` tokens
                 divided by factor, those of more than `high` turns left, those
                 between going over linearly in their turns."""
-    import math
     import torch
     if rot < 0 or rot % 2 or base <= 0 or factor <= 0 or kind not in ("none", "linear", "base", "parts"):
         raise ValueError(f"rope_frequencies: need even rot >= 0, base > 0, factor > 0 and a known kind (rot={rot} "

@@ -142,3 +142,21 @@ def test_empty_and_refused():
     row = torch.randn((4, 6, 128), device=dev).half()
     want = wq.rope(row[:, :2], p, f)
     assert torch.equal(wq.rope(row[:, :2], p, f, out=row[:, 2:4]), want)
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_out_beside_x_in_every_head(layout):
+    """x and out as the two halves of each head's row, and as alternating heads."""
+    dev = device()
+    rng = np.random.default_rng(8)
+    T, H, dim = 5, 6, 64
+    x = rng.standard_normal((T, H, dim)).astype(np.float16)
+    pos = to_dev(np.arange(T, dtype=np.int32) * 1000)
+    freqs = wq.rope_frequencies(dim)
+    want = wq.rope(to_dev(x), pos, freqs, layout)
+    for buf, a, b in ((torch.full((T, H, 2 * dim), 9.0, dtype=torch.float16, device=dev), np.s_[..., :dim], np.s_[..., dim:]),
+                      (torch.full((T, 2 * H, dim), 9.0, dtype=torch.float16, device=dev), np.s_[:, ::2], np.s_[:, 1::2])):
+        buf[a] = to_dev(x)
+        note(f"rope out beside x {layout}")
+        got = wq.rope(buf[a], pos, freqs, layout, out=buf[b])
+        assert torch.equal(got, want) and torch.equal(buf[a], to_dev(x))

@@ -199,3 +199,32 @@ def test_attention_rows_past_a_grid(heads, group, n):
     assert attend(c=c, n=n, qh=qh, qs=qh * 128, os_=qh * 128) == UNSUP
     assert b"workspace" in wq.load().wq_last_error()
     assert wq.load().wq_kv_paged_workspace_size(c, n, qh, ctypes.byref(need)) == OK
+
+
+def test_rows_meet_against_the_addresses():
+    """Whether two strided [tokens, heads, channels] views share an element, by
+    their addresses: never denied where they do, and not claimed for rows or heads
+    that lie side by side."""
+    torch = pytest.importorskip("torch")
+    meet = wq._rows_meet
+    base = torch.zeros(4096, dtype=torch.float16)
+
+    def cells(t):
+        at = t.storage_offset()
+        return {at + i * t.stride(0) + h * t.stride(1) + c for i in range(t.shape[0]) for h in range(t.shape[1])
+                for c in range(t.shape[2])}
+
+    rng = np.random.default_rng(1)
+    for _ in range(3000):
+        T, H, D = (int(rng.integers(1, n)) for n in (5, 5, 9))
+        views = [base.as_strided((T, H, D), (int(rng.integers(0, 60)), int(rng.integers(0, 30)), 1),
+                                 int(rng.integers(0, 100))) for _ in range(2)]
+        if cells(views[0]) & cells(views[1]):
+            assert meet(*views) and meet(*views[::-1])
+    x = base[:3 * 4 * 32].view(3, 4, 32)
+    for a, b in ((x[..., :16], x[..., 16:]), (x[:, :2], x[:, 2:]), (x[:, ::2], x[:, 1::2]), (x[..., 4:12], x[..., 20:28]),
+                 (x[:1], x[1:2])):
+        assert not cells(a) & cells(b)
+        assert not meet(a, b) and not meet(b, a)
+    for a, b in ((x, x), (x[..., :17], x[..., 15:]), (x[:, :2], x[:, 1:3]), (x[:2], x[1:])):
+        assert cells(a) & cells(b) and meet(a, b)
