@@ -842,8 +842,9 @@ wq_status wq_kv_paged_compact(const wq_kv_paged* cache, const int32_t* lens, voi
     if (!lens || !table_out || !used) return fail(WQ_ERR_INVALID_ARG, "wq_kv_paged_compact: null pointer");
     if (!aligned(lens, 4) || !aligned(table_out, 4) || !aligned(used, 4))
         return fail(WQ_ERR_MISALIGNED, "wq_kv_paged_compact: lens, table_out and used need 4-byte alignment");
-    if (table_out == cache->table)
-        return fail(WQ_ERR_INVALID_ARG, "wq_kv_paged_compact: table_out must not be the cache's table");
+    const uintptr_t from = reinterpret_cast<uintptr_t>(cache->table), to = reinterpret_cast<uintptr_t>(table_out);
+    if ((from < to ? to - from : from - to) / sizeof(int32_t) < (uintptr_t)(a.slots * a.max_pages))
+        return fail(WQ_ERR_INVALID_ARG, "wq_kv_paged_compact: table_out must not overlap the cache's table");
     return check_hip(wq::launch_paged_compact(a, lens, static_cast<int32_t*>(table_out), used, workspace, num_cus(),
                                               static_cast<hipStream_t>(stream)),
                      "wq_kv_paged_compact launch");

@@ -559,9 +559,10 @@ wq_status wq_kv_paged_fork(const wq_kv_paged* cache, int32_t* lens, const int32_
  * stays, and the others take the free ones in ascending order.  table_out
  * int32 [slots][max_pages] receives the new table (entries that are no whole
  * block, or name no page, become -1) and used int32 [1] the number of pages in
- * use; the cache's own table is only read, and pages in use lie where they lay
- * before as well, until the caller writes there.  The caller then goes on with
- * table_out; every page from `used` on is free.
+ * use; the cache's own table is only read (table_out must not overlap it:
+ * WQ_ERR_INVALID_ARG), and pages in use lie where they lay before as well,
+ * until the caller writes there.  The caller then goes on with table_out; every
+ * page from `used` on is free.
  * Needs a workspace (wq_kv_paged_compact_workspace_size).
  */
 wq_status wq_kv_paged_compact(const wq_kv_paged* cache, const int32_t* lens, void* table_out,

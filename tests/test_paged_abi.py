@@ -228,3 +228,12 @@ def test_rows_meet_against_the_addresses():
         assert not meet(a, b) and not meet(b, a)
     for a, b in ((x, x), (x[..., :17], x[..., 15:]), (x[:, :2], x[:, 1:3]), (x[:2], x[1:])):
         assert cells(a) & cells(b) and meet(a, b)
+
+
+def test_compact_table_over_the_cache_s_refused():
+    for off in (4, -4, 156, -156):                 # 8 slots of 5 entries: 160 bytes
+        assert compact(out=FAKE + off) == BAD, off
+        assert b"overlap" in wq.load().wq_last_error()
+    assert compact(out=FAKE + 156, ws=0, wn=0) == BAD
+    wide = paged(slots=(1 << 31) - 1, max_pages=(1 << 24) - 1)
+    assert compact(c=ctypes.byref(wide), out=FAKE + (1 << 40)) == BAD and b"overlap" in wq.load().wq_last_error()
