@@ -6,8 +6,11 @@
 // z = round(-min / s), c = clamp(round(x / s) + z)), K per channel and V per
 // token (§7 "axis choice"), deciding every rounding as exact arithmetic would.
 //
-// What bounds it: a call with many blocks, the encoding's instructions and HBM
-// about alike (16 prompts with 8 heads, 31 MB: 14 us); a decode step, the chain
+// What bounds it: a call with many blocks, vector instructions and waiting (64
+// prompts of 4096 tokens with 8 heads, 1.36 GB: 414 us, 3.3 TB/s; by counters 61 % of
+// the SIMDs' cycles are vector instructions, 18 a value, of which the encoding is
+// six; codes leave in 32-byte pieces, half a row each, though no byte twice; 16
+// prompts, 31 MB: 14 us); a decode step, the chain
 // of dependent reads of lens, window and table (64 sequences, one of which
 // completes a block, 8 heads: 6.5 us, 3.2 where none does).  Whole blocks are
 // therefore quantized in quarters of 256 threads, which start within the time
@@ -406,8 +409,9 @@ struct Pairs {
 };
 
 // Page bytes are contiguous over the heads: thread by thread one 16-byte vector,
-// loaded past the caches and stored through them.  400 pages of 139264 bytes at
-// 18.2 us, 6.1 TB/s; both sides cached 26.3, four vectors a thread 20.2.
+// loaded past the caches and stored through them.  400 pages of 139264 bytes take
+// 20.6 us (median; 19.0 the least), 5.4 TB/s.  (When this was chosen: 18.2, against
+// 26.3 with both sides cached and 20.2 with four vectors a thread.)
 __global__ __launch_bounds__(kThreads) void paged_copy_kernel(const PagedArgs c, const Pairs pairs) {
     const int2 p = pairs.p[blockIdx.y];
     const int64_t vecs = c.heads * (kRecord / 16), at = (int64_t)blockIdx.x * kThreads + threadIdx.x;

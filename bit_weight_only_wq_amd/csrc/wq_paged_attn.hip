@@ -3,9 +3,12 @@
 // ("What actually happens when you quantize a KV cache", §2 the decode step,
 // §3-§4 the codec, §7 "axis choice").
 //
-// What bounds it: HBM.  A token of a KV head is 136 bytes and is read once for
-// all the query heads of its group, so both products run on the matrix cores,
-// with the group's heads as the 16 columns of v_mfma_f32_16x16x32_f16.
+// What bounds it: HBM for groups of up to 4 query heads; from there on start and
+// join, and the vector instructions of the softmax and of the factors' halves.  A
+// token of a KV head is 136 bytes and is read once for up to 16 query heads of its
+// group (larger groups are several rows, and each reads it), so both products run
+// on the matrix cores, with those heads as the 16 columns of
+// v_mfma_f32_16x16x32_f16.
 //
 // Work is cut into units of about 17 KB: one page record (128 tokens of one KV
 // head), or 32 tokens of a window.  The units of all entries stand in one line
@@ -41,8 +44,10 @@
 // 16 c 2^-24 everywhere (two more shifts): the hardware adds products of c
 // 2^-24 to a sum with less of their lower bits (measured over 64 products of
 // positive numbers: 4e-6 off, all one way, against 2.4e-7 for 16 c 2^-24 and
-// for normal numbers), which a score bears (it is at most 1e-5 off) but a long
-// sum of positive weights does not.
+// for normal numbers), which a long sum of positive weights does not bear.  A score
+// is a sum of 128 and softmax takes differences of scores: equal scores, in
+// blocks with and without zero points and in the window, came out less than 1e-6 of
+// the sum of their terms' magnitudes apart.
 // The zero points enter as sum a_d z_d (a product with the zeros as B, once per
 // unit) and sum w_t z_t (in fp32, per lane): any fp16 value, as a scale may be.
 //
@@ -61,10 +66,12 @@
 // of the largest.
 //
 // Measured, kernel and join together: 32 sequences of 4096 tokens with 32 heads
-// of their own (571 MB) 100 us, 5.7 TB/s; one of 131149 tokens with 64 query
-// heads on 8 (143 MB) 39 us, 3.7 TB/s; 64 of lengths from 0 to 16384 with the
-// same heads (142 MB) 45 us; one of 500 tokens with 32 heads 10.8 us, which is a
-// launch and one workgroup's chain of dependent reads.
+// of their own (571 MB) 101 us, 5.7 TB/s; one of 131149 tokens with 64 query
+// heads on 8 (143 MB) 40 us, 3.6 TB/s; 64 of lengths from 0 to 16384 with the
+// same heads (142 MB) 46 us; one of 500 tokens with 32 heads 10.8 us, which is a
+// launch and one workgroup's chain of dependent reads.  32 sequences of 8192
+// tokens and 8 KV heads (287 to 294 MB) with groups of 12 heads 72 us, 16 74, 24
+// 126 (two rows), 64 239 (four rows).
 #include "wq_paged.h"
 
 namespace wq {
@@ -1071,9 +1078,11 @@ hipError_t launch_paged_attention(const void* q, int64_t q_stride, int64_t q_hea
     const int64_t rows = count * c.heads * A.chunks, most = rows * (c.max_pages + 4);
     const int64_t groups = num_cus < most ? num_cus : most;
     // A few rows of at most 16 units: one workgroup each, two units a wave, and
-    // no second kernel (32 rows of 7 units 12.0 us instead of 14.2; with more
+    // no second kernel (32 rows of 7 units 10.7 us instead of 13.0; with more
     // rows than compute units the equal runs win, 4096 rows of 2 units 80 us
-    // instead of 152).
+    // instead of 152).  The lengths lie on the device, so the rule takes the most
+    // that the table's width lets them be: short sequences in a cache made for long
+    // ones have the runs and the join.
     const bool short_rows = c.max_pages + 4 <= 16 && rows <= num_cus;
     const size_t cross_bytes = (size_t)(groups + 1) * sizeof(int4);
     const size_t parts = (size_t)groups * 2 * A.per_chunk;
