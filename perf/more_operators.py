@@ -1,0 +1,251 @@
+"""Cases of the 8-bit path's operators: the root-mean-square norm with the
+residual's addition, the quantization of rows to 8 bits, and the product of
+8-bit activations and weights.
+
+A case is measured through the library's entry points (own = True) or in the
+plain form below (own = False).
+
+Codes are int8 in [-127, 127] with one fp32 scale per row (a token of the
+activations, an output channel of the weights): value = code * scale.  Every
+code is decided as the exact quotient decides it, ties to even, so codes are
+whole numbers that any two implementations agree on, and are returned as such
+beside their scales.
+"""
+
+import math
+
+import torch
+
+own = False
+
+DEV = "cuda"
+TYPES = {"fp16": torch.float16, "bf16": torch.bfloat16}
+EPS = 1e-6
+
+
+# ---- the cases ---------------------------------------------------------------
+
+def listed():
+    return [
+        # Norms.  One token of one sequence of a 7B model, the smallest call:
+        # the residual is added, the codes go to the q/k/v products.
+        dict(name="norm_one_token", op="norm", rows=1, K=4096, dtype="fp16", residual=True, codes=True),
+        # A decode batch of a 70B model whose products take 16-bit activations
+        # (weight-only codes): the norm's values, no codes.
+        dict(name="norm_batch_values", op="norm", rows=64, K=8192, dtype="bf16", residual=True, codes=False),
+        # An odd number of packed tokens of a small model, first layer: nothing
+        # to add.
+        dict(name="norm_ragged", op="norm", rows=1777, K=896, dtype="fp16", residual=False, codes=True),
+        # A long prompt through a 70B model's layer.
+        dict(name="norm_prompt", op="norm", rows=8192, K=8192, dtype="fp16", residual=True, codes=True),
+        # Rows.  The attention's output of a few prompts, for the output product.
+        dict(name="rows_attention", op="rows", rows=333, K=4096, dtype="bf16", gate=False),
+        # The gated values of a 70B model's feed-forward layer, for its down
+        # product: a decode batch.
+        dict(name="gated_batch", op="rows", rows=64, K=28672, dtype="fp16", gate=True),
+        # The same of a 7B model, a long prompt.
+        dict(name="gated_prompt", op="rows", rows=8192, K=11008, dtype="bf16", gate=True),
+        # A 70B model's up-projection brought to 8 bits: one scale per output channel.
+        dict(name="rows_weights", op="rows", rows=28672, K=8192, dtype="fp16", gate=False),
+        # Products.  One token through a 7B model's q, k, v or o matrix.
+        dict(name="product_one_token", op="product", M=1, K=4096, N=4096, dtype="fp16", bias=False),
+        # A decode batch through a 70B model's up-projection.
+        dict(name="product_batch", op="product", M=64, K=8192, N=28672, dtype="fp16", bias=False),
+        # A few packed prompts through a 7B model's down-projection.
+        dict(name="product_ragged", op="product", M=333, K=11008, N=4096, dtype="bf16", bias=True),
+        # A long prompt through a 70B model's up-projection.
+        dict(name="product_prompt", op="product", M=8192, K=8192, N=28672, dtype="bf16", bias=False),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def _width(rng, lo, hi):
+    """A model's width: one in use, or any in between, odd ones among them."""
+    return rng.choice([w for w in (896, 4096, 4864, 8192, 11008, 28672) if lo <= w <= hi] + [_log(rng, lo, hi)] * 3)
+
+
+def draw(rng):
+    op = rng.choice(["norm", "rows", "product", "product"])
+    dtype = rng.choice(["fp16", "bf16"])
+    if op == "norm":
+        K = _width(rng, 64, 16384)
+        return dict(op=op, rows=_log(rng, 1, min(16384, 8192 * 8192 // K)), K=K, dtype=dtype,
+                    residual=rng.random() < 0.75, codes=rng.random() < 0.75)
+    if op == "rows":
+        K, gate = _width(rng, 64, 28672), rng.random() < 0.5
+        most = 8192 * 11008 if gate else 28672 * 8192
+        return dict(op=op, rows=_log(rng, 1, min(32768, most // K)), K=K, dtype=dtype, gate=gate)
+    K = (_width(rng, 64, 28672) + 15) // 16 * 16
+    N = _width(rng, 16, 28672)
+    return dict(op=op, M=_log(rng, 1, min(8192, 8192 * 8192 * 28672 // (K * N))), K=K, N=N, dtype=dtype,
+                bias=rng.random() < 0.5)
+
+
+def work(case):
+    """Bytes and operations that one pass cannot do without."""
+    if case["op"] == "product":
+        M, K, N = case["M"], case["K"], case["N"]
+        return {"bytes": M * K + N * K + 2 * M * N + 4 * M + 4 * N + (2 * N if case["bias"] else 0),
+                "flops": 2 * M * N * K}
+    n = case["rows"] * case["K"]
+    if case["op"] == "norm":
+        return {"bytes": (2 + (4 if case["residual"] else 0) + (1 if case["codes"] else 2)) * n + 2 * case["K"]
+                + (4 * case["rows"] if case["codes"] else 0), "flops": 5 * n}
+    return {"bytes": (5 if case["gate"] else 3) * n + 4 * case["rows"], "flops": (6 if case["gate"] else 2) * n}
+
+
+# ---- the inputs --------------------------------------------------------------
+
+def _gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def _randn(g, *shape):
+    return torch.randn(shape, generator=g, device=DEV)
+
+
+def _codes(g, rows, K):
+    """int8 [rows, K] as normal values have them: the largest of some thousands
+    lies near four standard deviations."""
+    return (_randn(g, rows, K) * 31.0).round_().clamp_(-127, 127).to(torch.int8)
+
+
+def prepare(case, seed):
+    g, dtype = _gen(seed), TYPES[case["dtype"]]
+    st = dict(op=case["op"], dtype=dtype)
+    if case["op"] == "norm":
+        R, K = case["rows"], case["K"]
+        x = _randn(g, R, K)
+        res = None
+        if case["residual"]:                    # a residual stream has a few large channels
+            res = _randn(g, R, K) * 4.0
+            res[:, :: max(1, K // 5)] *= 20.0
+            res = res.to(dtype)
+        st.update(x=x.to(dtype), weight=(1.0 + 0.2 * _randn(g, K)).to(dtype), residual=res, codes=case["codes"])
+        return st
+    if case["op"] == "rows":
+        R, K = case["rows"], case["K"]
+        x = _randn(g, R, 2 * K if case["gate"] else K).to(dtype)   # gate and up side by side, as one product gives them
+        st.update(x=x[:, -K:], gate=x[:, :K] if case["gate"] else None)
+        return st
+    M, K, N = case["M"], case["K"], case["N"]
+    st.update(a=_codes(g, M, K), w=_codes(g, N, K),
+              a_scales=(0.5 + torch.rand(M, generator=g, device=DEV)) * 0.03,
+              w_scales=(0.5 + torch.rand(N, generator=g, device=DEV)) * 0.0005,
+              bias=_randn(g, N).to(dtype) if case["bias"] else None)
+    return st
+
+
+# ---- one pass ----------------------------------------------------------------
+
+def run(st):
+    return _kernels(st) if own else _PLAIN[st["op"]](st)
+
+
+def _kernels(st):
+    import bit_weight_only_wq_amd as wq
+    if st["op"] == "norm":
+        if not st["codes"]:
+            y, total = wq.rmsnorm(st["x"], st["weight"], residual=st["residual"], eps=EPS)
+            return {"values": y, "total": total}
+        codes, scales, total = wq.rmsnorm_quantize(st["x"], st["weight"], residual=st["residual"], eps=EPS)
+        return {"codes": codes, "scales": scales, "total": total}
+    if st["op"] == "rows":
+        codes, scales = wq.quantize_rows(st["x"], gate=st["gate"])
+        return {"codes": codes, "scales": scales}
+    if "workspace" not in st:
+        st["workspace"] = wq.gemm_w8a8_workspace(st["a"].shape[0], st["w"].shape[0], st["a"].shape[1])
+    return wq.gemm_w8a8(st["a"], st["a_scales"], st["w"], st["w_scales"], bias=st["bias"], dtype=st["dtype"],
+                        workspace=st["workspace"])
+
+
+def _round_codes(t, top):
+    """Codes of t [rows, K] with the rows' largest magnitudes top [rows, 1].  64
+    bits: a quotient next to a border between two codes falls on its own side."""
+    return torch.round(127 * t.double() / torch.where(top == 0, 1.0, top.double())).to(torch.int8)
+
+
+def _plain_norm(st):
+    x, total = st["x"].float(), None
+    if st["residual"] is not None:
+        total = (x + st["residual"].float()).to(st["dtype"])
+        x = total.float()
+    r = 1.0 / torch.sqrt((x * x).mean(1, keepdim=True) + EPS)
+    t = x * st["weight"].float()                # exact: two 16-bit values
+    if not st["codes"]:
+        return {"values": (t * r).to(st["dtype"]), "total": total}
+    top = t.abs().amax(1, keepdim=True)
+    scales = torch.where(top == 0, 1.0, top * r / 127)
+    return {"codes": _round_codes(t, top), "scales": scales[:, 0], "total": total}
+
+
+def _plain_rows(st):
+    y = st["x"].float()
+    if st["gate"] is not None:                  # 64 bits: codes are decided on unrounded values
+        gate = st["gate"].double()
+        y = y * (gate / (1 + torch.exp(-gate)))
+    top = y.abs().amax(1, keepdim=True)
+    scales = torch.where(top == 0, 1.0, top / 127).float()
+    return {"codes": _round_codes(y, top), "scales": scales[:, 0]}
+
+
+def _plain_product(st):
+    y = torch.matmul(st["a"].float(), st["w"].float().t())
+    y = y * st["a_scales"][:, None] * st["w_scales"]
+    if st["bias"] is not None:
+        y = y + st["bias"].float()
+    return y.to(st["dtype"])
+
+
+_PLAIN = {"norm": _plain_norm, "rows": _plain_rows, "product": _plain_product}
+
+
+# ---- the definitions in 64 bits ------------------------------------------------
+
+def _nearest_codes(t):
+    """round-half-even(127 t / max|t|) of each row from whole comparisons: the
+    code k is the largest with (2 k - 1) max <= 254 |t|, one less if that is
+    an equality and k odd."""
+    top = t.abs().amax(1, keepdim=True)
+    two = torch.where(top == 0, 1.0, 2 * top)
+    over = 254 * t.abs() + top
+    k = torch.floor(over / two)
+    k = k - ((k * two == over) & (k % 2 == 1)).double()
+    return (k * torch.sign(t)).to(torch.int8), top[:, 0]
+
+
+def _exact_norm(st):
+    h = st["x"].double()
+    if st["residual"] is not None:
+        h = (h + st["residual"].double()).to(st["dtype"]).double()
+    total = h if st["residual"] is not None else None
+    rms = (h.square().sum(1) / h.shape[1] + EPS).sqrt()
+    t = h * st["weight"].double()
+    if not st["codes"]:
+        return {"values": t / rms[:, None], "total": total}
+    codes, top = _nearest_codes(t)
+    return {"codes": codes, "scales": torch.where(top == 0, 1.0, top / rms / 127), "total": total}
+
+
+def _exact_rows(st):
+    y = st["x"].double()
+    if st["gate"] is not None:
+        g = st["gate"].double()
+        e = torch.exp(-g.abs())                 # 1 / (1 + exp(-g)) without a large exponential
+        y = y * g * torch.where(g < 0, e, 1.0) / (1 + e)
+    codes, top = _nearest_codes(y)
+    return {"codes": codes, "scales": torch.where(top == 0, 1.0, top / 127)}
+
+
+def _exact_product(st):
+    y = torch.mm(st["a"].double(), st["w"].double().t())
+    y = y * (st["a_scales"].double()[:, None] * st["w_scales"].double())
+    return y if st["bias"] is None else y + st["bias"].double()
+
+
+def exact(case, seed):
+    """From the definitions, in 64 bits."""
+    return {"norm": _exact_norm, "rows": _exact_rows, "product": _exact_product}[case["op"]](prepare(case, seed))
