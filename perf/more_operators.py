@@ -9,7 +9,9 @@ Codes are int8 in [-127, 127] with one fp32 scale per row (a token of the
 activations, an output channel of the weights): value = code * scale.  Every
 code is decided as the exact quotient decides it, ties to even, so codes are
 whole numbers that any two implementations agree on, and are returned as such
-beside their scales.
+beside their scales.  (A gated row has a tie where a value's gate is that of the
+largest and their ratio is a tie's: 64 bits come within 2^-44 of it, and what
+lies within 2^-40 of a tie counts as one.)
 """
 
 import math
@@ -165,7 +167,9 @@ def _kernels(st):
 def _round_codes(t, top):
     """Codes of t [rows, K] with the rows' largest magnitudes top [rows, 1].  64
     bits: a quotient next to a border between two codes falls on its own side."""
-    return torch.round(127 * t.double() / torch.where(top == 0, 1.0, top.double())).to(torch.int8)
+    q = 127 * t.double() / torch.where(top == 0, 1.0, top.double())
+    half = torch.round(2 * q) / 2
+    return torch.round(torch.where((q - half).abs() < 2.0 ** -40, half, q)).to(torch.int8)
 
 
 def _plain_norm(st):
@@ -208,12 +212,12 @@ _PLAIN = {"norm": _plain_norm, "rows": _plain_rows, "product": _plain_product}
 def _nearest_codes(t):
     """round-half-even(127 t / max|t|) of each row from whole comparisons: the
     code k is the largest with (2 k - 1) max <= 254 |t|, one less if that is
-    an equality and k odd."""
+    an equality and k odd (within 2^-40 of max, see above)."""
     top = t.abs().amax(1, keepdim=True)
     two = torch.where(top == 0, 1.0, 2 * top)
     over = 254 * t.abs() + top
-    k = torch.floor(over / two)
-    k = k - ((k * two == over) & (k % 2 == 1)).double()
+    k = torch.floor(over / two + 2.0 ** -40)
+    k = k - (((k * two - over).abs() <= two * 2.0 ** -40) & (k % 2 == 1)).double()
     return (k * torch.sign(t)).to(torch.int8), top[:, 0]
 
 
