@@ -21,7 +21,7 @@ from ._lib import (WQ_PATH_AUTO, WQ_PATH_GEMV, WQ_PATH_MFMA, WQError,  # noqa: F
 __all__ = ["quantize_pack", "gemm", "gemm_grouped", "gemm_workspace_bytes", "codes_bytes", "num_groups",
            "gemv_max_batch",
            "gemm_nf4", "gemm_offset", "KVCache", "kv_quantize_block", "kv_attention",
-           "rope", "rope_frequencies", "PagedKV", "kv_paged_append", "kv_paged_attention", "kv_paged_workspace",
+           "rope", "rope_frequencies", "quantize_rows", "rmsnorm_quantize", "rmsnorm", "gemm_w8a8", "gemm_w8a8_workspace", "PagedKV", "kv_paged_append", "kv_paged_attention", "kv_paged_workspace",
            "kv_paged_copy", "kv_paged_fork", "kv_paged_compact", "kv_paged_compact_workspace",
            "WQError", "LIB_PATH", "load"]
 
@@ -454,6 +454,194 @@ def rope(x, positions, freqs, layout: str = "half", scale: float = 1.0, out=None
     xs, os_ = x.stride(), out.stride()
     _launch("wq_rope", dev, load().wq_rope, x.data_ptr(), T, H, dim, xs[0], xs[1], positions.data_ptr(),
             freqs.data_ptr(), 2 * freqs.shape[0], ROPE_LAYOUTS[layout], scale, out.data_ptr(), os_[0], os_[1])
+    return out
+
+
+# ---- the 8-bit path -------------------------------------------------------------
+
+def _dtype(t, name):
+    """The 16-bit type of GPU tensor t and wq.h's number for it."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dtype == torch.float16:
+        return t.dtype, 0
+    if t.dtype == torch.bfloat16:
+        return t.dtype, 1
+    raise ValueError(f"{name} must be float16 or bfloat16, got {t.dtype}")
+
+
+def _rows2(t, dtype, rows, K, name, device):
+    """Checks [rows, K] with contiguous rows; returns the row stride."""
+    _gpu(t, dtype, name, device)
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or t.shape[1] != K or (K > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [{rows if rows is not None else 'rows'}, {K}] with contiguous rows, got "
+                         f"{tuple(t.shape)} of strides {t.stride()}")
+    return t.stride(0) if t.shape[0] > 1 else K
+
+
+def _apart(a, b, names):
+    """Refuses tensors (of 1 or 2 dimensions, rows contiguous) that share memory.
+    Rows of one stride that lie side by side are apart."""
+    if not a.numel() or not b.numel():
+        return
+    def shape(t):
+        n, st = (t.shape[0], t.stride(0)) if t.dim() == 2 else (1, 0)
+        return t.data_ptr(), n, st * t.element_size(), t.shape[-1] * t.element_size()
+    (pa, na, sa, ra), (pb, nb, sb, rb) = shape(a), shape(b)
+    d = pb - pa
+    if d >= (na - 1) * sa + ra or -d >= (nb - 1) * sb + rb:
+        return
+    if na > 1 and nb > 1 and sa == sb and ra <= d % sa <= sa - rb:
+        return
+    raise ValueError(f"{names[0]} overlaps {names[1]}")
+
+
+def _codes_out(out, rows, K, device, inputs):
+    """(codes, scales, stride) of a call: new, or the caller's."""
+    import torch
+    if out is None:
+        return (torch.empty((rows, K), dtype=torch.int8, device=device),
+                torch.empty(rows, dtype=torch.float32, device=device), K)
+    codes, scales = out
+    stride = _rows2(codes, torch.int8, rows, K, "codes", device)
+    _line(scales, torch.float32, rows, "scales", device)
+    _apart(codes, scales, ("codes", "scales"))
+    for t, name in inputs:
+        if t is not None:
+            _apart(codes, t, ("codes", name))
+            _apart(scales, t, ("scales", name))
+    return codes, scales, stride
+
+
+def quantize_rows(x, gate=None, out=None):
+    """Rows to 8 bits: x fp16 or bf16 [rows, K] -> (codes int8 [rows, K], scales
+    fp32 [rows]), value = code * scale.  With a gate of x's shape and type the
+    rows are x * silu(gate); both may be strided parts of one packed row.  out: a
+    (codes, scales) pair to write into; rows of codes may be strided.  A row of
+    zeros has scale 1, one with an infinity or a NaN codes 0 and scale NaN."""
+    dt, code = _dtype(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D [rows, K]")
+    rows, K = x.shape
+    dev = x.device
+    xs = _rows2(x, dt, rows, K, "x", dev)
+    gs = _rows2(gate, dt, rows, K, "gate", dev) if gate is not None else 0
+    codes, scales, cs = _codes_out(out, rows, K, dev, ((x, "x"), (gate, "gate")))
+    _launch("wq_quantize_rows", dev, load().wq_quantize_rows, x.data_ptr(), xs,
+            gate.data_ptr() if gate is not None else None, gs, rows, K, code, codes.data_ptr(), cs, scales.data_ptr())
+    return codes, scales
+
+
+def _norm_inputs(x, weight, residual, total):
+    """Checks a norm's inputs; (dtype code, rows, K, x stride, residual pointer and
+    stride, total, its pointer and stride)."""
+    import torch
+    dt, code = _dtype(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D [rows, K]")
+    rows, K = x.shape
+    dev = x.device
+    xs = _rows2(x, dt, rows, K, "x", dev)
+    _line(weight, dt, K, "weight", dev)
+    if residual is None:
+        if total is not None:
+            raise ValueError("total goes with a residual")
+        return code, rows, K, xs, None, 0, None, None, 0
+    rs = _rows2(residual, dt, rows, K, "residual", dev)
+    if total is None:
+        total = torch.empty((rows, K), dtype=dt, device=dev)
+        ts = K
+    else:
+        ts = _rows2(total, dt, rows, K, "total", dev)
+        _apart(total, weight, ("total", "weight"))
+        for t, st, name in ((x, xs, "x"), (residual, rs, "residual")):
+            if not (total.data_ptr() == t.data_ptr() and ts == st):
+                _apart(total, t, ("total", name))
+    return code, rows, K, xs, residual.data_ptr(), rs, total, total.data_ptr(), ts
+
+
+def rmsnorm_quantize(x, weight, residual=None, eps: float = 1e-6, total=None, out=None):
+    """Root-mean-square norm of rows in 8 bits: with h = x + residual (rounded to
+    x's type; fp16 or bf16 [rows, K]) the rows h * weight / sqrt(mean(h^2) + eps)
+    as (codes int8 [rows, K], scales fp32 [rows], total).  total is h, the next
+    residual: new, or written into the given tensor, which may be x or residual
+    itself; None without a residual.  out: a (codes, scales) pair."""
+    code, rows, K, xs, rp, rs, total, tp, ts = _norm_inputs(x, weight, residual, total)
+    dev = x.device
+    codes, scales, cs = _codes_out(out, rows, K, dev, ((x, "x"), (weight, "weight"), (residual, "residual"),
+                                                       (total, "total")))
+    _launch("wq_rmsnorm_quantize", dev, load().wq_rmsnorm_quantize, x.data_ptr(), xs, rp, rs, weight.data_ptr(), rows, K,
+            code, eps, tp, ts, codes.data_ptr(), cs, scales.data_ptr())
+    return codes, scales, total
+
+
+def rmsnorm(x, weight, residual=None, eps: float = 1e-6, total=None, out=None):
+    """rmsnorm_quantize with the norm's values in x's type, for products of 16-bit
+    activations: returns (y, total).  out: a tensor of x's shape."""
+    import torch
+    code, rows, K, xs, rp, rs, total, tp, ts = _norm_inputs(x, weight, residual, total)
+    dev = x.device
+    if out is None:
+        out = torch.empty((rows, K), dtype=x.dtype, device=dev)
+        os_ = K
+    else:
+        os_ = _rows2(out, x.dtype, rows, K, "out", dev)
+        for t, name in ((x, "x"), (weight, "weight"), (residual, "residual"), (total, "total")):
+            if t is not None:
+                _apart(out, t, ("out", name))
+    _launch("wq_rmsnorm", dev, load().wq_rmsnorm, x.data_ptr(), xs, rp, rs, weight.data_ptr(), rows, K, code, eps, tp, ts,
+            out.data_ptr(), os_)
+    return out, total
+
+
+def gemm_w8a8_workspace(B: int, N: int, K: int, device="cuda"):
+    """A workspace tensor for gemm_w8a8 calls of this shape that do not overlap
+    (uint8, possibly empty)."""
+    import torch
+    with torch.cuda.device(device):
+        need = _size_t(load().wq_gemm_w8a8_workspace_size, B, K, N, where="wq_gemm_w8a8")
+    return torch.empty(need, dtype=torch.uint8, device=device)
+
+
+def gemm_w8a8(a, a_scales, w, w_scales, bias=None, dtype=None, out=None, workspace=None, use_workspace=True):
+    """Y [B, N] = a int8 [B, K] times w int8 [N, K] transposed, times a_scales fp32
+    [B] and w_scales fp32 [N], plus bias [N]: operands as quantize_rows and
+    rmsnorm_quantize give them (w: quantize_rows of the weights), K a multiple of
+    16, rows 16-byte aligned.  Y (and bias) is of dtype, float16 or bfloat16: that
+    of bias or out if not given, else float16.  Results are the same bits whatever
+    the batch and the workspace.  The workspace comes from torch or from
+    `workspace` (gemm_w8a8_workspace); use_workspace=False does without."""
+    import torch
+    if not isinstance(a, torch.Tensor) or a.dim() != 2 or not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise ValueError("a must be int8 [B, K] and w int8 [N, K]")
+    B, K = a.shape
+    N = w.shape[0]
+    dev = a.device
+    as_ = _rows2(a, torch.int8, B, K, "a", dev)
+    ws_ = _rows2(w, torch.int8, N, K, "w", dev)
+    _line(a_scales, torch.float32, B, "a_scales", dev)
+    _line(w_scales, torch.float32, N, "w_scales", dev)
+    if dtype is None:
+        dtype = bias.dtype if bias is not None else out.dtype if out is not None else torch.float16
+    if dtype is not torch.float16 and dtype is not torch.bfloat16:
+        raise ValueError(f"dtype must be float16 or bfloat16, got {dtype}")
+    if bias is not None:
+        _line(bias, dtype, N, "bias", dev)
+    if out is None:
+        out = torch.empty((B, N), dtype=dtype, device=dev)
+        ys = N
+    else:
+        ys = _rows2(out, dtype, B, N, "out", dev)
+        for t, name in ((a, "a"), (w, "w"), (a_scales, "a_scales"), (w_scales, "w_scales"), (bias, "bias")):
+            if t is not None:
+                _apart(out, t, ("out", name))
+    if workspace is None and use_workspace:
+        workspace = gemm_w8a8_workspace(B, N, K, dev)
+    wp, wn = _given(workspace, dev) if workspace is not None and use_workspace else (None, 0)
+    _launch("wq_gemm_w8a8", dev, load().wq_gemm_w8a8, a.data_ptr(), as_, a_scales.data_ptr(), w.data_ptr(), ws_,
+            w_scales.data_ptr(), bias.data_ptr() if bias is not None else None, out.data_ptr(), ys, B, K, N,
+            1 if dtype is torch.bfloat16 else 0, wp, wn)
     return out
 
 

@@ -27,6 +27,9 @@ WQ_SCHEME_OFFSET = 4
 WQ_ROPE_HALF = 0
 WQ_ROPE_INTERLEAVED = 1
 
+WQ_FP16 = 0
+WQ_BF16 = 1
+
 WQ_KV_RECORD_BYTES = 17408
 
 # Every symbol include/wq.h declares, with (restype, argtypes).
@@ -72,6 +75,12 @@ SIGNATURES = {
     "wq_kv_workspace_size": (ctypes.c_int, [ctypes.POINTER(KvCache), ctypes.POINTER(_SZ)]),
     "wq_rope": (ctypes.c_int, [_P, _I64, _I64, _I64, _I64, _I64, _P, _P, _I64, _I32, ctypes.c_float, _P,
                                _I64, _I64, _P]),
+    "wq_quantize_rows": (ctypes.c_int, [_P, _I64, _P, _I64, _I64, _I64, _I32, _P, _I64, _P, _P]),
+    "wq_rmsnorm_quantize": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _I64, _I32, ctypes.c_float, _P, _I64,
+                                           _P, _I64, _P, _P]),
+    "wq_rmsnorm": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _I64, _I32, ctypes.c_float, _P, _I64, _P, _I64, _P]),
+    "wq_gemm_w8a8": (ctypes.c_int, [_P, _I64, _P, _P, _I64, _P, _P, _P, _I64, _I64, _I64, _I64, _I32, _P, _SZ, _P]),
+    "wq_gemm_w8a8_workspace_size": (ctypes.c_int, [_I64, _I64, _I64, ctypes.POINTER(_SZ)]),
     "wq_kv_paged_append": (ctypes.c_int, [_P, _P, _I64, _I64, _I64, _PAGED, _P, _P, _P, _I64, _P]),
     "wq_kv_paged_attention": (ctypes.c_int, [_P, _I64, _I64, _PAGED, _P, _P, _I64, _I64, ctypes.c_float, _P,
                                              _I64, _P, _SZ, _P]),

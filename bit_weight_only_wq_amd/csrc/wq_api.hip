@@ -628,6 +628,144 @@ wq_status wq_rope(const void* x, int64_t tokens, int64_t heads, int64_t dim, int
     return check_hip(wq::launch_rope(c, num_cus(), static_cast<hipStream_t>(stream)), "wq_rope launch");
 }
 
+// ---- 8-bit path ------------------------------------------------------------------
+
+// Rows of K values `stride` elements apart; an output's rows may not overlap.
+static bool row_strides_ok(int64_t rows, int64_t K, int64_t stride, bool output) {
+    return stride >= 0 && stride <= (int64_t)1 << 37 && (!output || rows <= 1 || stride >= K);
+}
+
+static wq_status check_rows_shape(const char* who, int64_t rows, int64_t K, int32_t dtype) {
+    if (rows < 0 || K < 1 || (dtype != WQ_FP16 && dtype != WQ_BF16)) {
+        snprintf(g_last_error, sizeof(g_last_error), "%s: need rows >= 0, K >= 1 and a known dtype (rows=%lld K=%lld "
+                 "dtype=%d)", who, (long long)rows, (long long)K, (int)dtype);
+        return WQ_ERR_INVALID_ARG;
+    }
+    if (rows >= (int64_t)1 << 24 || K > (int64_t)1 << 20) {
+        snprintf(g_last_error, sizeof(g_last_error), "%s: rows < 2^24 and K <= 2^20 (rows=%lld K=%lld)", who,
+                 (long long)rows, (long long)K);
+        return WQ_ERR_UNSUPPORTED;
+    }
+    return WQ_OK;
+}
+
+static wq_status run_norm(const char* who, const wq::NormCall& c, int32_t dtype, void* stream) {
+    g_last_error[0] = '\0';
+    const wq_status st = check_rows_shape(who, c.rows, c.K, dtype);
+    if (st != WQ_OK) return st;
+    if (!(c.eps >= 0x1p-126f) || c.eps > 3.4e38f)
+        return fail(WQ_ERR_INVALID_ARG, "rmsnorm: eps must be finite and at least 2^-126");
+    if (!row_strides_ok(c.rows, c.K, c.x_stride, false) || !row_strides_ok(c.rows, c.K, c.residual_stride, false) ||
+        !row_strides_ok(c.rows, c.K, c.total_stride, c.total) || !row_strides_ok(c.rows, c.K, c.codes_stride, c.codes) ||
+        !row_strides_ok(c.rows, c.K, c.out_stride, c.out))
+        return fail(WQ_ERR_INVALID_ARG, "rmsnorm: strides must be in [0, 2^37], an output's at least K=%lld", c.K);
+    if (c.rows == 0) return WQ_OK;
+    if (!c.x || !c.weight || !(c.codes ? (const void*)c.scales : c.out)) {
+        snprintf(g_last_error, sizeof(g_last_error), "%s: null pointer", who);
+        return WQ_ERR_INVALID_ARG;
+    }
+    if (!c.residual != !c.total)
+        return fail(WQ_ERR_INVALID_ARG, "rmsnorm: residual and total go together");
+    if (c.total && c.rows > 1 && ((c.total == c.x && c.total_stride != c.x_stride) ||
+                                  (c.total == c.residual && c.total_stride != c.residual_stride)))
+        return fail(WQ_ERR_INVALID_ARG, "rmsnorm: in place needs equal strides");
+    if (!aligned(c.x, 2) || !aligned(c.residual, 2) || !aligned(c.weight, 2) || !aligned(c.total, 2) ||
+        !aligned(c.out, 2) || !aligned(c.scales, 4))
+        return fail(WQ_ERR_MISALIGNED, "rmsnorm: 16-bit arrays need 2-byte, scales 4-byte alignment");
+    return check_hip(wq::launch_norm(c, static_cast<hipStream_t>(stream)), "rmsnorm launch");
+}
+
+wq_status wq_rmsnorm_quantize(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                              const void* weight, int64_t rows, int64_t K, int32_t dtype, float eps, void* total,
+                              int64_t total_stride, void* codes, int64_t codes_stride, float* scales, void* stream) {
+    // (a null codes must not pass for a call of wq_rmsnorm)
+    if (!codes && rows > 0) return fail(WQ_ERR_INVALID_ARG, "wq_rmsnorm_quantize: null pointer");
+    const wq::NormCall c{x, residual, weight, total, codes, scales, nullptr, rows, K, x_stride, residual_stride,
+                         total_stride, codes_stride, 0, eps, dtype == WQ_BF16};
+    return run_norm("wq_rmsnorm_quantize", c, dtype, stream);
+}
+
+wq_status wq_rmsnorm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                     const void* weight, int64_t rows, int64_t K, int32_t dtype, float eps, void* total,
+                     int64_t total_stride, void* out, int64_t out_stride, void* stream) {
+    const wq::NormCall c{x, residual, weight, total, nullptr, nullptr, out, rows, K, x_stride, residual_stride,
+                         total_stride, 0, out_stride, eps, dtype == WQ_BF16};
+    return run_norm("wq_rmsnorm", c, dtype, stream);
+}
+
+wq_status wq_quantize_rows(const void* x, int64_t x_stride, const void* gate, int64_t gate_stride, int64_t rows,
+                           int64_t K, int32_t dtype, void* codes, int64_t codes_stride, float* scales, void* stream) {
+    g_last_error[0] = '\0';
+    const wq_status st = check_rows_shape("wq_quantize_rows", rows, K, dtype);
+    if (st != WQ_OK) return st;
+    if (!row_strides_ok(rows, K, x_stride, false) || !row_strides_ok(rows, K, gate_stride, false) ||
+        !row_strides_ok(rows, K, codes_stride, true))
+        return fail(WQ_ERR_INVALID_ARG, "wq_quantize_rows: strides must be in [0, 2^37], that of codes at least K=%lld", K);
+    if (rows == 0) return WQ_OK;
+    if (!x || !codes || !scales) return fail(WQ_ERR_INVALID_ARG, "wq_quantize_rows: null pointer");
+    if (!aligned(x, 2) || !aligned(gate, 2) || !aligned(scales, 4))
+        return fail(WQ_ERR_MISALIGNED, "wq_quantize_rows: x and gate need 2-byte, scales 4-byte alignment");
+    const wq::RowsCall c{x, gate, codes, scales, rows, K, x_stride, gate_stride, codes_stride, dtype == WQ_BF16};
+    return check_hip(wq::launch_rows(c, static_cast<hipStream_t>(stream)), "wq_quantize_rows launch");
+}
+
+static wq_status check_w8_shape(int64_t B, int64_t K, int64_t N) {
+    if (B < 0 || N < 0 || K < 1)
+        return fail(WQ_ERR_INVALID_ARG, "wq_gemm_w8a8: need B, N >= 0 and K >= 1 (B=%lld K=%lld)", B, K);
+    if (K % 16 != 0 || K >= (int64_t)1 << 17)
+        return fail(WQ_ERR_UNSUPPORTED, "wq_gemm_w8a8: K must be a multiple of 16 below 2^17 (K=%lld)", K);
+    if (B > (int64_t)1 << 20 || N > (int64_t)1 << 24)
+        return fail(WQ_ERR_UNSUPPORTED, "wq_gemm_w8a8: B <= 2^20 and N <= 2^24 (B=%lld N=%lld)", B, N);
+    return WQ_OK;
+}
+
+wq_status wq_gemm_w8a8_workspace_size(int64_t B, int64_t K, int64_t N, size_t* bytes) {
+    g_last_error[0] = '\0';
+    if (!bytes) return fail(WQ_ERR_INVALID_ARG, "wq_gemm_w8a8_workspace_size: null bytes");
+    *bytes = 0;
+    const wq_status st = check_w8_shape(B, K, N);
+    if (st != WQ_OK || B == 0 || N == 0) return st;
+    wq::W8Call c{};
+    c.B = B;
+    c.K = K;
+    c.N = N;
+    size_t need = 0;
+    wq::Scratch ws;
+    ws.need = &need;
+    const hipError_t e = wq::launch_gemm_w8(c, num_cus(), ws, nullptr);
+    if (e != hipSuccess) return check_hip(e, "wq_gemm_w8a8_workspace_size");
+    *bytes = need;
+    return WQ_OK;
+}
+
+wq_status wq_gemm_w8a8(const void* A, int64_t a_stride, const float* a_scales, const void* W, int64_t w_stride,
+                       const float* w_scales, const void* bias, void* Y, int64_t y_stride, int64_t B, int64_t K,
+                       int64_t N, int32_t dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    g_last_error[0] = '\0';
+    size_t need = 0;
+    wq_status st = wq_gemm_w8a8_workspace_size(B, K, N, &need);
+    if (st != WQ_OK) return st;
+    if (dtype != WQ_FP16 && dtype != WQ_BF16)
+        return fail(WQ_ERR_INVALID_ARG, "wq_gemm_w8a8: unknown dtype %lld", dtype);
+    const int64_t far = (int64_t)1 << 22;
+    if ((B > 1 && (a_stride < K || y_stride < N)) || (N > 1 && w_stride < K) || a_stride < 0 || w_stride < 0 ||
+        y_stride < 0 || a_stride > far || w_stride > far || y_stride > (int64_t)1 << 37)
+        return fail(WQ_ERR_INVALID_ARG, "wq_gemm_w8a8: a_stride and w_stride must be in [K, 2^22], y_stride in [N, 2^37] "
+                    "(K=%lld N=%lld)", K, N);
+    if (B == 0 || N == 0) return WQ_OK;
+    if (!A || !a_scales || !W || !w_scales || !Y) return fail(WQ_ERR_INVALID_ARG, "wq_gemm_w8a8: null pointer");
+    if (!aligned(A, 16) || !aligned(W, 16) || a_stride % 16 != 0 || w_stride % 16 != 0 || !aligned(a_scales, 4) ||
+        !aligned(w_scales, 4) || !aligned(bias, 2) || !aligned(Y, 2))
+        return fail(WQ_ERR_MISALIGNED, "wq_gemm_w8a8: A, W and their strides need 16-byte, scales 4-byte, bias and Y "
+                    "2-byte alignment");
+    st = check_workspace("wq_gemm_w8a8", workspace, workspace_bytes, need);
+    if (st != WQ_OK) return st;
+    const wq::W8Call c{A, a_scales, W, w_scales, bias, Y, B, K, N, a_stride, w_stride, y_stride, dtype == WQ_BF16};
+    wq::Scratch ws;
+    ws.ptr = workspace;
+    return check_hip(wq::launch_gemm_w8(c, num_cus(), ws, static_cast<hipStream_t>(stream)), "wq_gemm_w8a8 launch");
+}
+
 // ---- paged KV cache --------------------------------------------------------------
 
 // Validates a descriptor's sizes, and the buffers named in `need` (1 pages,

@@ -202,4 +202,40 @@ size_t paged_compact_bytes(const PagedArgs& c);
 hipError_t launch_paged_compact(const PagedArgs& c, const int32_t* lens, int32_t* table_out, int32_t* used,
                                 void* scratch, int num_cus, hipStream_t stream);
 
+// Norm of rows, rows to 8 bits (wq_rows.hip), and the 8-bit product
+// (wq_gemm_w8.hip).  Strides in elements; bf16: the 16-bit type, else fp16.
+struct NormCall {
+    const void* x;
+    const void* residual;     // null: none
+    const void* weight;
+    void* total;              // null: not written
+    void* codes;              // codes and scales, or out
+    float* scales;
+    void* out;
+    int64_t rows, K, x_stride, residual_stride, total_stride, codes_stride, out_stride;
+    float eps;
+    bool bf16;
+};
+hipError_t launch_norm(const NormCall& c, hipStream_t stream);
+struct RowsCall {
+    const void* x;
+    const void* gate;         // null: none
+    void* codes;
+    float* scales;
+    int64_t rows, K, x_stride, gate_stride, codes_stride;
+    bool bf16;
+};
+hipError_t launch_rows(const RowsCall& c, hipStream_t stream);
+struct W8Call {
+    const void* A;
+    const float* a_scales;
+    const void* W;
+    const float* w_scales;
+    const void* bias;         // null: none
+    void* Y;
+    int64_t B, K, N, a_stride, w_stride, y_stride;
+    bool bf16;
+};
+hipError_t launch_gemm_w8(const W8Call& c, int num_cus, const Scratch& ws, hipStream_t stream);
+
 }  // namespace wq

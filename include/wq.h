@@ -435,6 +435,88 @@ wq_status wq_rope(const void* x, int64_t tokens, int64_t heads, int64_t dim, int
                   int32_t layout, float scale, void* out, int64_t out_token_stride,
                   int64_t out_head_stride, void* stream);
 
+/* 16-bit type of activations where a call takes either. */
+typedef enum {
+    WQ_FP16 = 0,
+    WQ_BF16 = 1
+} wq_dtype;
+
+/*
+ * The 8-bit path: past the ridge (prompts, large batches) the weights' bytes no
+ * longer bound a product, and 8-bit activations on 8-bit weights run at twice
+ * the matrix rate of 16-bit ones.  A row of activations (a token) or weights
+ * (an output channel) is held as
+ *     codes   int8 [rows][K], codes_stride elements from row to row
+ *     scales  fp32 [rows]
+ *     value = code * scale,  code = round-half-even(127 t / max|t|) in [-127, 127]
+ * where t are the row's values before the scale is taken out; every code is
+ * decided as the exact quotient decides it.  A row of zeros has codes 0 and
+ * scale 1.  A row that holds an infinity or a NaN, or whose t go past fp32's
+ * range, has codes 0 and scale NaN, so that what is computed from it shows it.
+ * dtype is the type of the 16-bit arrays of a call.
+ *
+ * wq_quantize_rows: t = x, or with a gate t = x * gate / (1 + exp(-gate)), formed
+ * in 64 bits where a code's border is near (nothing is rounded between gate and
+ * code; within 2^-40 of a tie counts as one); scales = max|t| / 127 (a quotient that is no fp32 number above 0 counts
+ * as a row of zeros).  x and gate may be the halves of one packed row.  It
+ * makes the other operands of the products of a layer, and weights: W [N][K]
+ * gives one scale for each output channel.  (Codes of wq_quantize_pack_ex with
+ * bits 8, group = K, WQ_SCHEME_SYM serve as well: flip each byte's top bit and
+ * widen the scales.)
+ *
+ * x, gate  16-bit [rows][K], 2-byte aligned, strides in elements in [0, 2^37]
+ * codes    stride >= K if rows > 1; scales 4-byte aligned
+ * 0 <= rows < 2^24, 1 <= K <= 2^20 (beyond: WQ_ERR_UNSUPPORTED).  With 16-byte
+ * aligned x and gate, 8-byte aligned codes, and K and the strides multiples of
+ * 8, loads and stores are wide.  Inputs may be infinite or NaN.
+ */
+wq_status wq_quantize_rows(const void* x, int64_t x_stride, const void* gate, int64_t gate_stride, int64_t rows,
+                           int64_t K, int32_t dtype, void* codes, int64_t codes_stride, float* scales, void* stream);
+
+/*
+ * Root-mean-square norm of rows, with the residual's addition before it:
+ *     h = x + residual, rounded to the arrays' type and written to total
+ *     y = h * weight / sqrt(mean(h^2) + eps)
+ * Without a residual h = x, and total is not written (both are null then).
+ * wq_rmsnorm writes y, rounded once; wq_rmsnorm_quantize writes y in 8 bits
+ * (above, t = h * weight: the norm's factor is one for the row and cancels in
+ * the codes).  Squares are summed in 64 bits.
+ *
+ * x, residual, total, out  16-bit [rows][K], 2-byte aligned, strides as above;
+ *        total may be x or residual itself, at its stride
+ * weight 16-bit [K];  eps in [2^-126, fp32's largest]
+ * Sizes, wide loads and non-finite inputs as wq_quantize_rows (wq_rmsnorm: a NaN
+ * makes its row NaN, an infinity makes its place NaN and the row's others 0).
+ */
+wq_status wq_rmsnorm_quantize(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                              const void* weight, int64_t rows, int64_t K, int32_t dtype, float eps, void* total,
+                              int64_t total_stride, void* codes, int64_t codes_stride, float* scales, void* stream);
+wq_status wq_rmsnorm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                     const void* weight, int64_t rows, int64_t K, int32_t dtype, float eps, void* total,
+                     int64_t total_stride, void* out, int64_t out_stride, void* stream);
+
+/*
+ * Product of 8-bit activations and 8-bit weights:
+ *     Y[b, n] = a_scales[b] * w_scales[n] * sum_k A[b, k] * W[n, k] + bias[n]
+ * The sum is exact in int32, so results are the same bits whatever the batch,
+ * the split of the work or the workspace; it is converted to fp32, multiplied
+ * by a_scales, then by w_scales, bias is added, each rounded to fp32, and the
+ * result is rounded to Y's type.
+ *
+ * A, W     int8 [B][K] and [N][K], any values, 16-byte aligned; strides in
+ *          bytes, multiples of 16 in [K, 2^22]
+ * a_scales, w_scales fp32 [B], [N];  bias 16-bit [N] of Y's type, or null
+ * Y        16-bit [B][N] (dtype), 2-byte aligned, y_stride elements >= N
+ * B, N >= 0 (0 is a no-op), B <= 2^20, N <= 2^24; K a multiple of 16 below
+ * 2^17 (WQ_ERR_UNSUPPORTED otherwise).
+ * Workspace (wq_gemm_w8a8_workspace_size): int32 partial sums where K is split
+ * to fill the GPU; without one K is not split.
+ */
+wq_status wq_gemm_w8a8(const void* A, int64_t a_stride, const float* a_scales, const void* W, int64_t w_stride,
+                       const float* w_scales, const void* bias, void* Y, int64_t y_stride, int64_t B, int64_t K,
+                       int64_t N, int32_t dtype, void* workspace, size_t workspace_bytes, void* stream);
+wq_status wq_gemm_w8a8_workspace_size(int64_t B, int64_t K, int64_t N, size_t* bytes);
+
 /*
  * Paged int4 KV cache: the codec and blocks of wq_kv_cache, for many sequences
  * that grow one by one.  Head dimension 128, blocks of 128 tokens.
