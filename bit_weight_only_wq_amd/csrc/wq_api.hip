@@ -714,8 +714,8 @@ static wq_status check_w8_shape(int64_t B, int64_t K, int64_t N) {
         return fail(WQ_ERR_INVALID_ARG, "wq_gemm_w8a8: need B, N >= 0 and K >= 1 (B=%lld K=%lld)", B, K);
     if (K % 16 != 0 || K >= (int64_t)1 << 17)
         return fail(WQ_ERR_UNSUPPORTED, "wq_gemm_w8a8: K must be a multiple of 16 below 2^17 (K=%lld)", K);
-    if (B > (int64_t)1 << 20 || N > (int64_t)1 << 24)
-        return fail(WQ_ERR_UNSUPPORTED, "wq_gemm_w8a8: B <= 2^20 and N <= 2^24 (B=%lld N=%lld)", B, N);
+    if (B > (int64_t)1 << 20 || N > (int64_t)1 << 22)
+        return fail(WQ_ERR_UNSUPPORTED, "wq_gemm_w8a8: B <= 2^20 and N <= 2^22 (B=%lld N=%lld)", B, N);
     return WQ_OK;
 }
 
@@ -749,8 +749,8 @@ wq_status wq_gemm_w8a8(const void* A, int64_t a_stride, const float* a_scales, c
         return fail(WQ_ERR_INVALID_ARG, "wq_gemm_w8a8: unknown dtype %lld", dtype);
     const int64_t far = (int64_t)1 << 22;
     if ((B > 1 && (a_stride < K || y_stride < N)) || (N > 1 && w_stride < K) || a_stride < 0 || w_stride < 0 ||
-        y_stride < 0 || a_stride > far || w_stride > far || y_stride > (int64_t)1 << 37)
-        return fail(WQ_ERR_INVALID_ARG, "wq_gemm_w8a8: a_stride and w_stride must be in [K, 2^22], y_stride in [N, 2^37] "
+        y_stride < 0 || a_stride > far || w_stride > far || y_stride > far)
+        return fail(WQ_ERR_INVALID_ARG, "wq_gemm_w8a8: a_stride and w_stride must be in [K, 2^22], y_stride in [N, 2^22] "
                     "(K=%lld N=%lld)", K, N);
     if (B == 0 || N == 0) return WQ_OK;
     if (!A || !a_scales || !W || !w_scales || !Y) return fail(WQ_ERR_INVALID_ARG, "wq_gemm_w8a8: null pointer");
@@ -760,7 +760,9 @@ wq_status wq_gemm_w8a8(const void* A, int64_t a_stride, const float* a_scales, c
                     "2-byte alignment");
     st = check_workspace("wq_gemm_w8a8", workspace, workspace_bytes, need);
     if (st != WQ_OK) return st;
-    const wq::W8Call c{A, a_scales, W, w_scales, bias, Y, B, K, N, a_stride, w_stride, y_stride, dtype == WQ_BF16};
+    // (one row has no stride: the kernels' buffers end by it)
+    const wq::W8Call c{A, a_scales, W, w_scales, bias, Y, B, K, N, B > 1 ? a_stride : K, N > 1 ? w_stride : K,
+                       B > 1 ? y_stride : N, dtype == WQ_BF16};
     wq::Scratch ws;
     ws.ptr = workspace;
     return check_hip(wq::launch_gemm_w8(c, num_cus(), ws, static_cast<hipStream_t>(stream)), "wq_gemm_w8a8 launch");

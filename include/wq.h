@@ -506,8 +506,9 @@ wq_status wq_rmsnorm(const void* x, int64_t x_stride, const void* residual, int6
  * A, W     int8 [B][K] and [N][K], any values, 16-byte aligned; strides in
  *          bytes, multiples of 16 in [K, 2^22]
  * a_scales, w_scales fp32 [B], [N];  bias 16-bit [N] of Y's type, or null
- * Y        16-bit [B][N] (dtype), 2-byte aligned, y_stride elements >= N
- * B, N >= 0 (0 is a no-op), B <= 2^20, N <= 2^24; K a multiple of 16 below
+ * Y        16-bit [B][N] (dtype), 2-byte aligned, y_stride elements in
+ *          [N, 2^22]
+ * B, N >= 0 (0 is a no-op), B <= 2^20, N <= 2^22; K a multiple of 16 below
  * 2^17 (WQ_ERR_UNSUPPORTED otherwise).
  * Workspace (wq_gemm_w8a8_workspace_size): int32 partial sums where K is split
  * to fill the GPU; without one K is not split.

@@ -56,6 +56,20 @@ def test_models_products(B, K, N, dt):
     check(B, K, N, dt, N % 2 == 1)
 
 
+# Sizes past what one workgroup a compute unit covers, for every kind of tile:
+# few rows on wide matrices, splits of a long K, workgroups that take several
+# tiles (one step of K, an odd number of steps, a last step that is not whole).
+@pytest.mark.parametrize("B,K,N", [
+    (20, 304, 16500), (32, 512, 16640), (7, 1040, 9000), (60, 304, 16501), (49, 640, 9000), (40, 8192, 5200),
+    (700, 8208, 3000), (500, 8208, 2050), (130, 4112, 8200), (1025, 272, 8200), (2300, 272, 8200), (2300, 96, 8200),
+    (4300, 272, 8200), (4300, 112, 8195), (4300, 400, 8192), (300, 16, 20000), (20000, 16, 300), (20000, 144, 17),
+    (1100, 304, 2050), (2100, 1168, 2052), (600, 28672, 2050)])
+@pytest.mark.parametrize("dt,bias", [("fp16", False), ("bf16", True)])
+def test_many_tiles(B, K, N, dt, bias):
+    device()
+    check(B, K, N, dt, bias)
+
+
 @pytest.mark.parametrize("B,K,N", [(1, 131056, 33), (20, 131056, 65), (300, 131056, 129)])
 def test_largest_sums(B, K, N):
     """All of -128 * -128 (and of 127 * -128) over the longest K: just inside int32."""
