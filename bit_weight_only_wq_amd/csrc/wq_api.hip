@@ -681,7 +681,7 @@ wq_status wq_rmsnorm_quantize(const void* x, int64_t x_stride, const void* resid
     // (a null codes must not pass for a call of wq_rmsnorm)
     if (!codes && rows > 0) return fail(WQ_ERR_INVALID_ARG, "wq_rmsnorm_quantize: null pointer");
     const wq::NormCall c{x, residual, weight, total, codes, scales, nullptr, rows, K, x_stride, residual_stride,
-                         total_stride, codes_stride, 0, eps, dtype == WQ_BF16};
+                         total_stride, codes_stride, 0, K > 0 ? 1.0 / (double)K : 0.0, eps, dtype == WQ_BF16};
     return run_norm("wq_rmsnorm_quantize", c, dtype, stream);
 }
 
@@ -689,7 +689,7 @@ wq_status wq_rmsnorm(const void* x, int64_t x_stride, const void* residual, int6
                      const void* weight, int64_t rows, int64_t K, int32_t dtype, float eps, void* total,
                      int64_t total_stride, void* out, int64_t out_stride, void* stream) {
     const wq::NormCall c{x, residual, weight, total, nullptr, nullptr, out, rows, K, x_stride, residual_stride,
-                         total_stride, 0, out_stride, eps, dtype == WQ_BF16};
+                         total_stride, 0, out_stride, K > 0 ? 1.0 / (double)K : 0.0, eps, dtype == WQ_BF16};
     return run_norm("wq_rmsnorm", c, dtype, stream);
 }
 

@@ -213,6 +213,7 @@ struct NormCall {
     float* scales;
     void* out;
     int64_t rows, K, x_stride, residual_stride, total_stride, codes_stride, out_stride;
+    double per_value;         // 1 / K
     float eps;
     bool bf16;
 };

@@ -13,6 +13,8 @@
 // 2^-24 from it at least.  Gated values are off by some 2^-52 in fp64; they have
 // exact ties too (a value whose gate is that of the row's largest), so what lies
 // within 2^-40 of a border counts as on it.
+#include <type_traits>
+
 #include "wq_device.h"
 #include "wq_launch.h"
 
@@ -62,6 +64,13 @@ __device__ __forceinline__ int exact_code(double t, double top) {
     return (int)__builtin_rint(__builtin_fabs(q - half) < 0x1p-40 ? half : q);
 }
 
+// 1 / sqrt(mean h^2 + eps).  The mean is in 64 bits: bf16's squares may leave fp32's
+// range, and sums in another order then give the same factor (but once in 2^28 rows).
+__device__ __forceinline__ float norm_factor(const NormCall& A, double sum) {
+    const double mean = sum * A.per_value + (double)A.eps;
+    return mean > 0x1p-100 && mean < 0x1p100 ? 1.0f / __builtin_sqrtf((float)mean) : (float)(1.0 / sqrt(mean));
+}
+
 __device__ __forceinline__ double silu64(double g) { return g / (1.0 + exp(-g)); }
 
 // One workgroup a row, one value at a time; any size, stride and alignment.
@@ -84,19 +93,18 @@ __global__ __launch_bounds__(kThreads) void norm_any_kernel(const NormCall A) {
         sum += (double)v * (double)v;
     }
     block_join(top, sum);
-    const double r = 1.0 / sqrt(sum / (double)A.K + (double)A.eps);
-    const double t64 = (double)__builtin_bit_cast(float, top);
+    const float r = norm_factor(A, sum), amax = __builtin_bit_cast(float, top);
     const bool fine = top < kInfBits && sum < __builtin_inf();
     for (int64_t k = threadIdx.x; k < A.K; k += kThreads) {
         const float t = to_float(h[k], A.bf16) * to_float(w[k], A.bf16);
         if (A.out)
-            static_cast<uint16_t*>(A.out)[row * A.out_stride + k] = from_float(t * (float)r, A.bf16);
+            static_cast<uint16_t*>(A.out)[row * A.out_stride + k] = from_float(t * r, A.bf16);
         else
             static_cast<int8_t*>(A.codes)[row * A.codes_stride + k] =
-                fine && top ? (int8_t)exact_code((double)t, t64) : (int8_t)0;
+                fine && top ? (int8_t)exact_code((double)t, (double)amax) : (int8_t)0;
     }
     if (A.codes && threadIdx.x == 0)
-        A.scales[row] = !fine ? __builtin_nanf("") : top ? (float)(r * t64 / 127.0) : 1.0f;
+        A.scales[row] = !fine ? __builtin_nanf("") : top ? r * amax / 127.0f : 1.0f;
 }
 
 __global__ __launch_bounds__(kThreads) void rows_any_kernel(const RowsCall A) {
@@ -133,15 +141,333 @@ __global__ __launch_bounds__(kThreads) void rows_any_kernel(const RowsCall A) {
     if (threadIdx.x == 0) A.scales[row] = bads ? __builtin_nanf("") : scale == 0.0f ? 1.0f : scale;
 }
 
+// ---- 16-byte form --------------------------------------------------------------
+//
+// TPR threads take a row of up to 8 TPR VPT values, kept in registers from the one
+// load to the codes; a wave takes a row by itself where it is short (no meeting),
+// a workgroup where it is longer.
+
+enum { MODE_NORM_CODES, MODE_NORM_VALUES, MODE_ROWS, MODE_GATED };
+
+typedef unsigned int u4_t __attribute__((ext_vector_type(4)));
+
+template <bool BF16>
+__device__ __forceinline__ float part(u4_t v, int e) {
+    const uint32_t w = v[e >> 1];
+    if (BF16) return __builtin_bit_cast(float, e & 1 ? w & 0xFFFF0000u : w << 16);
+    return half_bits_to_float((uint16_t)(e & 1 ? w >> 16 : w));
+}
+
+template <bool BF16>
+__device__ __forceinline__ u4_t pack8(const float (&f)[8]) {
+    u4_t v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = (uint32_t)from_float(f[2 * i], BF16) | ((uint32_t)from_float(f[2 * i + 1], BF16) << 16);
+    return v;
+}
+
+// Largest bit pattern and sum over a row's TPR threads, in each of them.
+template <int TPR>
+__device__ __forceinline__ void row_join(uint32_t& top, double& sum, uint32_t* tops, double* sums) {
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+        const uint32_t t = __shfl_xor(top, o, kWave);
+        top = t > top ? t : top;
+        sum += __shfl_xor(sum, o, kWave);
+    }
+    if constexpr (TPR > kWave) {
+        if ((threadIdx.x & 63) == 0) {
+            tops[threadIdx.x >> 6] = top;
+            sums[threadIdx.x >> 6] = sum;
+        }
+        __syncthreads();
+        top = 0;
+        sum = 0.0;
+#pragma unroll
+        for (int w = 0; w < TPR / kWave; ++w) {
+            top = tops[w] > top ? tops[w] : top;
+            sum += sums[w];
+        }
+    }
+}
+
+template <int TPR>
+__device__ __forceinline__ double row_most(double v, double* mosts) {
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+        const double t = __shfl_xor(v, o, kWave);
+        v = t > v ? t : v;
+    }
+    if constexpr (TPR > kWave) {
+        if ((threadIdx.x & 63) == 0) mosts[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = 0.0;
+#pragma unroll
+        for (int w = 0; w < TPR / kWave; ++w) v = mosts[w] > v ? mosts[w] : v;
+    }
+    return v;
+}
+
+// x silu(g), off by less than 2^-20 of it for g >= -80: exp(-g) from its two parts
+// (whole and fraction of -g / ln 2, the product's own error added to the fraction).
+// Past 100 it is below fp32's half step next to 1.
+__device__ __forceinline__ float gated32(float x, float g) {
+    const float c = __builtin_fminf(g, 100.0f), hi = c * -1.44269502f;
+    const float lo = __builtin_fmaf(c, -1.44269502f, -hi) + c * -1.92596299e-8f;
+    const float n = __builtin_rintf(hi);
+    const float e = __builtin_ldexpf(__builtin_amdgcn_exp2f((hi - n) + lo), (int)n);
+    return x * (g * __builtin_amdgcn_rcpf(1.0f + e));
+}
+
+// Codes of eight values t, given 127 / top; those within `win` of a border are
+// decided by exact(i) in 64 bits.
+template <class F>
+__device__ __forceinline__ uint2 codes8(const float (&t)[8], float inv, float win, F exact) {
+    uint32_t z[8];
+    float far = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float q = t[i] * inv, r = q + 12582912.0f;            // 1.5 * 2^23: the sum's low bits are rint(q)
+        z[i] = __builtin_bit_cast(uint32_t, r);
+        far = __builtin_fmaxf(far, __builtin_fabsf(q - (r - 12582912.0f)));
+    }
+    if (!(far <= 0.5f - win)) {                                     // (a 0 times an infinite 127 / top among them)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float q = t[i] * inv;
+            if (!(__builtin_fabsf(q - __builtin_rintf(q)) <= 0.5f - win)) z[i] = (uint32_t)exact(i);
+        }
+    }
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        w[i] = __builtin_amdgcn_perm(z[4 * i + 1], z[4 * i], 0x0C0C0400u) |
+               __builtin_amdgcn_perm(z[4 * i + 3], z[4 * i + 2], 0x04000C0Cu);
+    return make_uint2(w[0], w[1]);
+}
+
+template <int MODE, bool BF16, int TPR, int VPT>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_vec_kernel(const NormCall A) {
+    constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
+    __shared__ uint32_t tops[TPR / kWave];
+    __shared__ double sums[TPR / kWave];
+    const int64_t row = (int64_t)blockIdx.x * RPB + (RPB > 1 ? threadIdx.x / TPR : 0);
+    if (RPB > 1 && row >= A.rows) return;                           // (a whole wave)
+    const int tid = threadIdx.x % TPR, nv = (int)(A.K >> 3);
+    const u4_t* x = reinterpret_cast<const u4_t*>(static_cast<const uint16_t*>(A.x) + row * A.x_stride);
+    const u4_t* res = reinterpret_cast<const u4_t*>(static_cast<const uint16_t*>(A.residual) + row * A.residual_stride);
+    const u4_t* wt = static_cast<const u4_t*>(A.weight);
+    u4_t* total = reinterpret_cast<u4_t*>(static_cast<uint16_t*>(A.total) + row * A.total_stride);
+    const bool add = A.residual != nullptr;
+    u4_t h[VPT], b[VPT], w[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int v = i * TPR + tid;
+        h[i] = b[i] = w[i] = u4_t{0, 0, 0, 0};
+        if (v < nv) {
+            h[i] = x[v];
+            if (add) b[i] = res[v];
+            w[i] = wt[v];
+        }
+    }
+    float t[VPT][8];
+    uint32_t top = 0;
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int v = i * TPR + tid;
+        if (add) {
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = part<BF16>(h[i], e) + part<BF16>(b[i], e);
+            h[i] = pack8<BF16>(f);
+            if (v < nv) total[v] = h[i];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float f = part<BF16>(h[i], e);
+            t[i][e] = f * part<BF16>(w[i], e);
+            const uint32_t u = __builtin_bit_cast(uint32_t, t[i][e]) & 0x7FFFFFFFu;
+            top = u > top ? u : top;
+            sum = __builtin_fma((double)f, (double)f, sum);
+        }
+    }
+    row_join<TPR>(top, sum, tops, sums);
+    const float r = norm_factor(A, sum);
+    if constexpr (MODE == MODE_NORM_VALUES) {
+        u4_t* out = reinterpret_cast<u4_t*>(static_cast<uint16_t*>(A.out) + row * A.out_stride);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = i * TPR + tid;
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = t[i][e] * r;
+            if (v < nv) out[v] = pack8<BF16>(f);
+        }
+        return;
+    }
+    const bool fine = top < kInfBits && sum < __builtin_inf();
+    const float amax = __builtin_bit_cast(float, top), inv = 127.0f / amax;
+    uint2* codes = reinterpret_cast<uint2*>(static_cast<int8_t*>(A.codes) + row * A.codes_stride);
+    const float win = amax < 0x1p-100f ? 1.0f : 0x1p-14f;           // (127 / amax may be infinite: all in 64 bits)
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int v = i * TPR + tid;
+        if (v >= nv) continue;
+        uint2 c = make_uint2(0, 0);
+        if (fine && top) c = codes8(t[i], inv, win, [&](int e) { return exact_code((double)t[i][e], (double)amax); });
+        codes[v] = c;
+    }
+    if (tid == 0) A.scales[row] = !fine ? __builtin_nanf("") : top ? r * amax / 127.0f : 1.0f;
+}
+
+template <int MODE, bool BF16, int TPR, int VPT>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rows_vec_kernel(const RowsCall A) {
+    constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
+    constexpr bool GATED = MODE == MODE_GATED;
+    __shared__ uint32_t tops[TPR / kWave];
+    __shared__ double sums[TPR / kWave], mosts[TPR / kWave];
+    const int64_t row = (int64_t)blockIdx.x * RPB + (RPB > 1 ? threadIdx.x / TPR : 0);
+    if (RPB > 1 && row >= A.rows) return;                           // (a whole wave)
+    const int tid = threadIdx.x % TPR, nv = (int)(A.K >> 3);
+    const u4_t* x = reinterpret_cast<const u4_t*>(static_cast<const uint16_t*>(A.x) + row * A.x_stride);
+    const u4_t* g = reinterpret_cast<const u4_t*>(static_cast<const uint16_t*>(A.gate) + row * A.gate_stride);
+    uint2* codes = reinterpret_cast<uint2*>(static_cast<int8_t*>(A.codes) + row * A.codes_stride);
+    u4_t xv[VPT], gv[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int v = i * TPR + tid;
+        xv[i] = gv[i] = u4_t{0, 0, 0, 0};
+        if (v < nv) {
+            xv[i] = x[v];
+            if (GATED) gv[i] = g[v];
+        }
+    }
+    // A value in 64 bits, from memory again where it is needed (seldom).
+    const auto value64 = [&](int v, int e) {
+        double y = (double)part<BF16>(x[v], e);
+        if (GATED) y *= silu64((double)part<BF16>(g[v], e));
+        return y;
+    };
+    float t[VPT][8];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            t[i][e] = part<BF16>(xv[i], e);
+            if (GATED) {
+                const float gate = part<BF16>(gv[i], e);
+                t[i][e] = gated32(t[i][e], gate);
+                // (exp(-gate) may leave fp32's range: the row goes in 64 bits)
+                top = gate < -80.0f ? 0x80000000u : top;
+            }
+            const uint32_t u = __builtin_bit_cast(uint32_t, t[i][e]) & 0x7FFFFFFFu;
+            top = u > top ? u : top;
+        }
+    double none = 0.0;
+    row_join<TPR>(top, none, tops, sums);
+    double most = (double)__builtin_bit_cast(float, top);
+    bool bad = top >= kInfBits;
+    const bool slow = GATED && (top >= 0x80000000u || top < 0x21800000u);   // 2^-60
+    if (GATED) {
+        // The largest magnitude in 64 bits: of the values near the largest in 32 (of
+        // all of the row's in the slow case).
+        double m = 0.0;
+        if (slow) {
+            bad = false;
+            for (int v = tid; v < nv; v += TPR)
+                for (int e = 0; e < 8; ++e) {
+                    const double y = __builtin_fabs(value64(v, e));
+                    m = !(y <= 3.4028234663852886e38) ? __builtin_inf() : y > m ? y : m;
+                }
+        } else if (!bad) {
+            const float near = __builtin_bit_cast(float, top) * (1.0f - 0x1p-18f);
+#pragma unroll
+            for (int i = 0; i < VPT; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (__builtin_fabsf(t[i][e]) >= near) {
+                        const double y = __builtin_fabs(value64(i * TPR + tid, e));
+                        m = y > m ? y : m;
+                    }
+        }
+        most = row_most<TPR>(m, mosts);
+        bad |= !(most <= 3.4028234663852886e38);
+    }
+    const bool zero = most <= 127 * 0x1p-150;                       // most / 127 rounds to 0
+    const float inv = 127.0f / (float)most;
+    const float win = slow || most < 0x1p-100 ? 1.0f : GATED ? 0x1p-12f : 0x1p-14f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int v = i * TPR + tid;
+        if (v >= nv) continue;
+        uint2 c = make_uint2(0, 0);
+        if (!bad && !zero)
+            c = codes8(t[i], inv, win, [&](int e) { return exact_code(GATED ? value64(v, e) : (double)t[i][e], most); });
+        codes[v] = c;
+    }
+    if (tid == 0) A.scales[row] = bad ? __builtin_nanf("") : zero ? 1.0f : (float)(most / 127.0);
+}
+
+bool by(const void* p, int64_t stride, int64_t bytes, int64_t size) {
+    return reinterpret_cast<uintptr_t>(p) % bytes == 0 && stride * size % bytes == 0;
+}
+
+// Runs f with the row's threads and vectors a thread as constants.
+template <class F>
+void with_width(int64_t K, F f) {
+    using std::integral_constant;
+    if (K <= 512) f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+    else if (K <= 1024) f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+    else if (K <= 2048) f(integral_constant<int, 256>{}, integral_constant<int, 1>{});
+    else if (K <= 4096) f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+    else if (K <= 8192) f(integral_constant<int, 256>{}, integral_constant<int, 4>{});
+    else if (K <= 16384) f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+    else f(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
+}
+
+template <int MODE, bool BF16>
+void run_norm_vec(const NormCall& c, hipStream_t stream) {
+    with_width(c.K, [&](auto tpr, auto vpt) {
+        constexpr int TPR = decltype(tpr)::value, VPT = decltype(vpt)::value, RPB = TPR < 256 ? 256 / TPR : 1;
+        norm_vec_kernel<MODE, BF16, TPR, VPT><<<dim3((unsigned)((c.rows + RPB - 1) / RPB)), dim3(TPR * RPB), 0, stream>>>(c);
+    });
+}
+
+template <int MODE, bool BF16>
+void run_rows_vec(const RowsCall& c, hipStream_t stream) {
+    with_width(c.K, [&](auto tpr, auto vpt) {
+        constexpr int TPR = decltype(tpr)::value, VPT = decltype(vpt)::value, RPB = TPR < 256 ? 256 / TPR : 1;
+        rows_vec_kernel<MODE, BF16, TPR, VPT><<<dim3((unsigned)((c.rows + RPB - 1) / RPB)), dim3(TPR * RPB), 0, stream>>>(c);
+    });
+}
+
 }  // namespace
 
+constexpr int64_t kWidest = 32768;   // values of a row that 1024 threads hold
+
 hipError_t launch_norm(const NormCall& c, hipStream_t stream) {
-    norm_any_kernel<<<dim3((unsigned)c.rows), dim3(kThreads), 0, stream>>>(c);
+    const bool vec = c.K % 8 == 0 && c.K <= kWidest && by(c.x, c.x_stride, 16, 2) && by(c.residual, c.residual_stride, 16, 2) &&
+                     by(c.weight, 0, 16, 2) && by(c.total, c.total_stride, 16, 2) && by(c.codes, c.codes_stride, 8, 1) &&
+                     by(c.out, c.out_stride, 16, 2);
+    if (!vec) norm_any_kernel<<<dim3((unsigned)c.rows), dim3(kThreads), 0, stream>>>(c);
+    else if (c.codes && c.bf16) run_norm_vec<MODE_NORM_CODES, true>(c, stream);
+    else if (c.codes) run_norm_vec<MODE_NORM_CODES, false>(c, stream);
+    else if (c.bf16) run_norm_vec<MODE_NORM_VALUES, true>(c, stream);
+    else run_norm_vec<MODE_NORM_VALUES, false>(c, stream);
     return hipGetLastError();
 }
 
 hipError_t launch_rows(const RowsCall& c, hipStream_t stream) {
-    rows_any_kernel<<<dim3((unsigned)c.rows), dim3(kThreads), 0, stream>>>(c);
+    const bool vec = c.K % 8 == 0 && c.K <= kWidest && by(c.x, c.x_stride, 16, 2) && by(c.gate, c.gate_stride, 16, 2) &&
+                     by(c.codes, c.codes_stride, 8, 1);
+    if (!vec) rows_any_kernel<<<dim3((unsigned)c.rows), dim3(kThreads), 0, stream>>>(c);
+    else if (c.gate && c.bf16) run_rows_vec<MODE_GATED, true>(c, stream);
+    else if (c.gate) run_rows_vec<MODE_GATED, false>(c, stream);
+    else if (c.bf16) run_rows_vec<MODE_ROWS, true>(c, stream);
+    else run_rows_vec<MODE_ROWS, false>(c, stream);
     return hipGetLastError();
 }
 
