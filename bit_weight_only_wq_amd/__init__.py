@@ -473,11 +473,27 @@ def _dtype(t, name):
 
 def _rows2(t, dtype, rows, K, name, device):
     """Checks [rows, K] with contiguous rows; returns the row stride."""
+    try:                                   # (the common case, told with few calls: one token's call counts them)
+        if t.dtype is dtype and t.device == device and t.shape == (rows, K):
+            st = t.stride()
+            if st[1] == 1:
+                return st[0] if rows > 1 else K
+    except AttributeError:
+        pass
     _gpu(t, dtype, name, device)
-    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or t.shape[1] != K or (K > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be [{rows if rows is not None else 'rows'}, {K}] with contiguous rows, got "
-                         f"{tuple(t.shape)} of strides {t.stride()}")
-    return t.stride(0) if t.shape[0] > 1 else K
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != K or (K > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [{rows}, {K}] with contiguous rows, got {tuple(t.shape)} of strides {t.stride()}")
+    return t.stride(0) if rows > 1 else K
+
+
+def _vector(t, dtype, n, name, device):
+    """_line, for calls of one token."""
+    try:
+        if t.dtype is dtype and t.device == device and t.shape == (n,) and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _line(t, dtype, n, name, device)
 
 
 def _apart(a, b, names):
@@ -497,15 +513,15 @@ def _apart(a, b, names):
     raise ValueError(f"{names[0]} overlaps {names[1]}")
 
 
-def _codes_out(out, rows, K, device, inputs):
+def _codes_out(out, x, rows, K, device, inputs):
     """(codes, scales, stride) of a call: new, or the caller's."""
     import torch
     if out is None:
-        return (torch.empty((rows, K), dtype=torch.int8, device=device),
-                torch.empty(rows, dtype=torch.float32, device=device), K)
+        # (like x: rows that are apart give contiguous ones)
+        return torch.empty_like(x, dtype=torch.int8), x.new_empty(rows, dtype=torch.float32), K
     codes, scales = out
     stride = _rows2(codes, torch.int8, rows, K, "codes", device)
-    _line(scales, torch.float32, rows, "scales", device)
+    _vector(scales, torch.float32, rows, "scales", device)
     _apart(codes, scales, ("codes", "scales"))
     for t, name in inputs:
         if t is not None:
@@ -527,7 +543,7 @@ def quantize_rows(x, gate=None, out=None):
     dev = x.device
     xs = _rows2(x, dt, rows, K, "x", dev)
     gs = _rows2(gate, dt, rows, K, "gate", dev) if gate is not None else 0
-    codes, scales, cs = _codes_out(out, rows, K, dev, ((x, "x"), (gate, "gate")))
+    codes, scales, cs = _codes_out(out, x, rows, K, dev, ((x, "x"), (gate, "gate")))
     _launch("wq_quantize_rows", dev, load().wq_quantize_rows, x.data_ptr(), xs,
             gate.data_ptr() if gate is not None else None, gs, rows, K, code, codes.data_ptr(), cs, scales.data_ptr())
     return codes, scales
@@ -543,14 +559,14 @@ def _norm_inputs(x, weight, residual, total):
     rows, K = x.shape
     dev = x.device
     xs = _rows2(x, dt, rows, K, "x", dev)
-    _line(weight, dt, K, "weight", dev)
+    _vector(weight, dt, K, "weight", dev)
     if residual is None:
         if total is not None:
             raise ValueError("total goes with a residual")
         return code, rows, K, xs, None, 0, None, None, 0
     rs = _rows2(residual, dt, rows, K, "residual", dev)
     if total is None:
-        total = torch.empty((rows, K), dtype=dt, device=dev)
+        total = torch.empty_like(x)
         ts = K
     else:
         ts = _rows2(total, dt, rows, K, "total", dev)
@@ -569,7 +585,7 @@ def rmsnorm_quantize(x, weight, residual=None, eps: float = 1e-6, total=None, ou
     itself; None without a residual.  out: a (codes, scales) pair."""
     code, rows, K, xs, rp, rs, total, tp, ts = _norm_inputs(x, weight, residual, total)
     dev = x.device
-    codes, scales, cs = _codes_out(out, rows, K, dev, ((x, "x"), (weight, "weight"), (residual, "residual"),
+    codes, scales, cs = _codes_out(out, x, rows, K, dev, ((x, "x"), (weight, "weight"), (residual, "residual"),
                                                        (total, "total")))
     _launch("wq_rmsnorm_quantize", dev, load().wq_rmsnorm_quantize, x.data_ptr(), xs, rp, rs, weight.data_ptr(), rows, K,
             code, eps, tp, ts, codes.data_ptr(), cs, scales.data_ptr())
@@ -583,7 +599,7 @@ def rmsnorm(x, weight, residual=None, eps: float = 1e-6, total=None, out=None):
     code, rows, K, xs, rp, rs, total, tp, ts = _norm_inputs(x, weight, residual, total)
     dev = x.device
     if out is None:
-        out = torch.empty((rows, K), dtype=x.dtype, device=dev)
+        out = torch.empty_like(x)
         os_ = K
     else:
         os_ = _rows2(out, x.dtype, rows, K, "out", dev)
@@ -620,16 +636,16 @@ def gemm_w8a8(a, a_scales, w, w_scales, bias=None, dtype=None, out=None, workspa
     dev = a.device
     as_ = _rows2(a, torch.int8, B, K, "a", dev)
     ws_ = _rows2(w, torch.int8, N, K, "w", dev)
-    _line(a_scales, torch.float32, B, "a_scales", dev)
-    _line(w_scales, torch.float32, N, "w_scales", dev)
+    _vector(a_scales, torch.float32, B, "a_scales", dev)
+    _vector(w_scales, torch.float32, N, "w_scales", dev)
     if dtype is None:
         dtype = bias.dtype if bias is not None else out.dtype if out is not None else torch.float16
     if dtype is not torch.float16 and dtype is not torch.bfloat16:
         raise ValueError(f"dtype must be float16 or bfloat16, got {dtype}")
     if bias is not None:
-        _line(bias, dtype, N, "bias", dev)
+        _vector(bias, dtype, N, "bias", dev)
     if out is None:
-        out = torch.empty((B, N), dtype=dtype, device=dev)
+        out = a.new_empty((B, N), dtype=dtype)
         ys = N
     else:
         ys = _rows2(out, dtype, B, N, "out", dev)

@@ -209,42 +209,69 @@ __device__ __forceinline__ double row_most(double v, double* mosts) {
     return v;
 }
 
-// x silu(g), off by less than 2^-20 of it for g >= -80: exp(-g) from its two parts
-// (whole and fraction of -g / ln 2, the product's own error added to the fraction).
-// Past 100 it is below fp32's half step next to 1.
+// x silu(g), off by at most 2^-21 of it for g >= -80 (two instructions of one step of
+// 2^-23, four roundings of 2^-24): exp(-g) as 2^hi (1 + lo ln 2), hi + lo = -g / ln 2
+// in two parts.  Past 100 it is below fp32's half step next to 1.
 __device__ __forceinline__ float gated32(float x, float g) {
     const float c = __builtin_fminf(g, 100.0f), hi = c * -1.44269502f;
-    const float lo = __builtin_fmaf(c, -1.44269502f, -hi) + c * -1.92596299e-8f;
-    const float n = __builtin_rintf(hi);
-    const float e = __builtin_ldexpf(__builtin_amdgcn_exp2f((hi - n) + lo), (int)n);
-    return x * (g * __builtin_amdgcn_rcpf(1.0f + e));
+    const float lo = __builtin_fmaf(c, -1.92596299e-8f, __builtin_fmaf(c, -1.44269502f, -hi));
+    const float e = __builtin_amdgcn_exp2f(hi);
+    return x * (g * __builtin_amdgcn_rcpf(1.0f + __builtin_fmaf(e * lo, 0.693147182f, e)));
 }
 
-// Codes of eight values t, given 127 / top; those within `win` of a border are
-// decided by exact(i) in 64 bits.
-template <class F>
-__device__ __forceinline__ uint2 codes8(const float (&t)[8], float inv, float win, F exact) {
+// Codes of eight values t, given 127 / top, and a bit for each that lies within
+// `win` of a border between two codes.
+__device__ __forceinline__ uint2 codes8(const float (&t)[8], float inv, float win, uint32_t& close) {
     uint32_t z[8];
-    float far = 0.0f;
+    float off[8], far = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float q = t[i] * inv, r = q + 12582912.0f;            // 1.5 * 2^23: the sum's low bits are rint(q)
+        const float r = __builtin_fmaf(t[i], inv, 12582912.0f);     // 1.5 * 2^23: the sum's low bits are the code
         z[i] = __builtin_bit_cast(uint32_t, r);
-        far = __builtin_fmaxf(far, __builtin_fabsf(q - (r - 12582912.0f)));
+        off[i] = __builtin_fmaf(t[i], inv, 12582912.0f - r);
+        far = __builtin_fmaxf(far, __builtin_fabsf(off[i]));
     }
-    if (!(far <= 0.5f - win)) {                                     // (a 0 times an infinite 127 / top among them)
+    close = 0;
+    if (!(far <= 0.5f - win))
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float q = t[i] * inv;
-            if (!(__builtin_fabsf(q - __builtin_rintf(q)) <= 0.5f - win)) z[i] = (uint32_t)exact(i);
-        }
-    }
+        for (int i = 0; i < 8; ++i) close |= !(__builtin_fabsf(off[i]) <= 0.5f - win) ? 1u << i : 0u;
     uint32_t w[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
         w[i] = __builtin_amdgcn_perm(z[4 * i + 1], z[4 * i], 0x0C0C0400u) |
                __builtin_amdgcn_perm(z[4 * i + 3], z[4 * i + 2], 0x04000C0Cu);
     return make_uint2(w[0], w[1]);
+}
+
+// The codes of a thread's vectors.  The few next to a border are decided in 64
+// bits after all are written, one after another from memory (value(k): the value
+// at place k of the row): vector by vector their waits add up (64 rows of 28672
+// gated values 12.7 instead of 11.6 us).
+template <int TPR, int VPT, class F>
+__device__ __forceinline__ void write_codes(const float (&t)[VPT][8], int8_t* codes, int nv, bool none, float top, double most,
+                                            float win, F value) {
+    static_assert(VPT <= 4, "a bit for each value");
+    const int tid = threadIdx.x % TPR;
+    // (127 / top may be infinite: all in 64 bits then)
+    const float inv = 127.0f / top;
+    win = top < 0x1p-100f ? 1.0f : win;
+    uint32_t close = 0;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int v = i * TPR + tid;
+        if (v >= nv) continue;
+        uint32_t near = 0;
+        uint2 c = make_uint2(0, 0);
+        if (!none) c = codes8(t[i], inv, win, near);
+        reinterpret_cast<uint2*>(codes)[v] = c;
+        close |= near << (8 * i);
+    }
+    while (close) {
+        const int bit = __builtin_ctz(close);
+        close &= close - 1;
+        const int k = ((bit >> 3) * TPR + tid) * 8 + (bit & 7);
+        codes[k] = (int8_t)exact_code(value(k), most);
+    }
 }
 
 template <int MODE, bool BF16, int TPR, int VPT>
@@ -308,17 +335,12 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_vec_kernel(const N
         return;
     }
     const bool fine = top < kInfBits && sum < __builtin_inf();
-    const float amax = __builtin_bit_cast(float, top), inv = 127.0f / amax;
-    uint2* codes = reinterpret_cast<uint2*>(static_cast<int8_t*>(A.codes) + row * A.codes_stride);
-    const float win = amax < 0x1p-100f ? 1.0f : 0x1p-14f;           // (127 / amax may be infinite: all in 64 bits)
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int v = i * TPR + tid;
-        if (v >= nv) continue;
-        uint2 c = make_uint2(0, 0);
-        if (fine && top) c = codes8(t[i], inv, win, [&](int e) { return exact_code((double)t[i][e], (double)amax); });
-        codes[v] = c;
-    }
+    const float amax = __builtin_bit_cast(float, top);
+    const uint16_t* from = reinterpret_cast<const uint16_t*>(add ? total : x);
+    write_codes<TPR>(t, static_cast<int8_t*>(A.codes) + row * A.codes_stride, nv, !fine || !top, amax, (double)amax, 0x1p-14f,
+                     [&](int k) {
+                         return (double)(to_float(from[k], BF16) * to_float(static_cast<const uint16_t*>(A.weight)[k], BF16));
+                     });
     if (tid == 0) A.scales[row] = !fine ? __builtin_nanf("") : top ? r * amax / 127.0f : 1.0f;
 }
 
@@ -333,7 +355,6 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rows_vec_kernel(const R
     const int tid = threadIdx.x % TPR, nv = (int)(A.K >> 3);
     const u4_t* x = reinterpret_cast<const u4_t*>(static_cast<const uint16_t*>(A.x) + row * A.x_stride);
     const u4_t* g = reinterpret_cast<const u4_t*>(static_cast<const uint16_t*>(A.gate) + row * A.gate_stride);
-    uint2* codes = reinterpret_cast<uint2*>(static_cast<int8_t*>(A.codes) + row * A.codes_stride);
     u4_t xv[VPT], gv[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -345,12 +366,12 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rows_vec_kernel(const R
         }
     }
     // A value in 64 bits, from memory again where it is needed (seldom).
-    const auto value64 = [&](int v, int e) {
-        double y = (double)part<BF16>(x[v], e);
-        if (GATED) y *= silu64((double)part<BF16>(g[v], e));
+    const auto value64 = [&](int k) {
+        double y = (double)to_float(reinterpret_cast<const uint16_t*>(x)[k], BF16);
+        if (GATED) y *= silu64((double)to_float(reinterpret_cast<const uint16_t*>(g)[k], BF16));
         return y;
     };
-    float t[VPT][8];
+    float t[VPT][8], least = 0.0f;
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
@@ -360,12 +381,13 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rows_vec_kernel(const R
             if (GATED) {
                 const float gate = part<BF16>(gv[i], e);
                 t[i][e] = gated32(t[i][e], gate);
-                // (exp(-gate) may leave fp32's range: the row goes in 64 bits)
-                top = gate < -80.0f ? 0x80000000u : top;
+                least = __builtin_fminf(least, gate);
             }
             const uint32_t u = __builtin_bit_cast(uint32_t, t[i][e]) & 0x7FFFFFFFu;
             top = u > top ? u : top;
         }
+    const float mine = __builtin_bit_cast(float, top);
+    if (GATED && least < -80.0f) top = 0x80000000u;                 // (exp(-gate) may leave fp32's range: the row goes in 64 bits)
     double none = 0.0;
     row_join<TPR>(top, none, tops, sums);
     double most = (double)__builtin_bit_cast(float, top);
@@ -377,37 +399,31 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rows_vec_kernel(const R
         double m = 0.0;
         if (slow) {
             bad = false;
-            for (int v = tid; v < nv; v += TPR)
-                for (int e = 0; e < 8; ++e) {
-                    const double y = __builtin_fabs(value64(v, e));
-                    m = !(y <= 3.4028234663852886e38) ? __builtin_inf() : y > m ? y : m;
-                }
-        } else if (!bad) {
+            for (int k = tid; k < 8 * nv; k += TPR) {
+                const double y = __builtin_fabs(value64(k));
+                m = !(y <= 3.4028234663852886e38) ? __builtin_inf() : y > m ? y : m;
+            }
+        } else if (!bad && mine >= __builtin_bit_cast(float, top) * (1.0f - 0x1p-18f)) {
             const float near = __builtin_bit_cast(float, top) * (1.0f - 0x1p-18f);
+            uint32_t close = 0;
 #pragma unroll
             for (int i = 0; i < VPT; ++i)
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (__builtin_fabsf(t[i][e]) >= near) {
-                        const double y = __builtin_fabs(value64(i * TPR + tid, e));
-                        m = y > m ? y : m;
-                    }
+                for (int e = 0; e < 8; ++e) close |= __builtin_fabsf(t[i][e]) >= near ? 1u << (8 * i + e) : 0u;
+            while (close) {
+                const int bit = __builtin_ctz(close);
+                close &= close - 1;
+                const double y = __builtin_fabs(value64(((bit >> 3) * TPR + tid) * 8 + (bit & 7)));
+                m = y > m ? y : m;
+            }
         }
         most = row_most<TPR>(m, mosts);
         bad |= !(most <= 3.4028234663852886e38);
     }
     const bool zero = most <= 127 * 0x1p-150;                       // most / 127 rounds to 0
-    const float inv = 127.0f / (float)most;
-    const float win = slow || most < 0x1p-100 ? 1.0f : GATED ? 0x1p-12f : 0x1p-14f;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int v = i * TPR + tid;
-        if (v >= nv) continue;
-        uint2 c = make_uint2(0, 0);
-        if (!bad && !zero)
-            c = codes8(t[i], inv, win, [&](int e) { return exact_code(GATED ? value64(v, e) : (double)t[i][e], most); });
-        codes[v] = c;
-    }
+    // (gated32 is off by 2^-21 at most, a quotient by 2^-14; in the slow case every code is decided in 64 bits)
+    write_codes<TPR>(t, static_cast<int8_t*>(A.codes) + row * A.codes_stride, nv, bad || zero, slow ? 0.0f : (float)most, most,
+                     GATED ? 0x1p-13f : 0x1p-14f, value64);
     if (tid == 0) A.scales[row] = bad ? __builtin_nanf("") : zero ? 1.0f : (float)(most / 127.0);
 }
 
@@ -415,7 +431,14 @@ bool by(const void* p, int64_t stride, int64_t bytes, int64_t size) {
     return reinterpret_cast<uintptr_t>(p) % bytes == 0 && stride * size % bytes == 0;
 }
 
-// Runs f with the row's threads and vectors a thread as constants.
+// Runs f with the row's threads and vectors a thread as constants: two vectors a
+// thread, so that several workgroups a compute unit wait for memory by turns.
+// 8192 rows of 8192 with a residual: 512 threads of two 86 us (5.4 TB/s), 256 of four
+// 94, 1024 of one 95; of 11008, gated: 512 of three 97 us (4.6 TB/s), 1024 of two 129,
+// 256 of six 315 (they spill); of 4096: 256 of two 46 us, 512 of one 48, a wave of
+// eight 121; 28672 rows of 8192 without norm 118 us, 6.0 TB/s.  What bounds the norm
+// and the plain rows is HBM, the gated ones the vector units as well (some 30
+// instructions a value).
 template <class F>
 void with_width(int64_t K, F f) {
     using std::integral_constant;
@@ -423,8 +446,9 @@ void with_width(int64_t K, F f) {
     else if (K <= 1024) f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
     else if (K <= 2048) f(integral_constant<int, 256>{}, integral_constant<int, 1>{});
     else if (K <= 4096) f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
-    else if (K <= 8192) f(integral_constant<int, 256>{}, integral_constant<int, 4>{});
-    else if (K <= 16384) f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+    else if (K <= 8192) f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
+    else if (K <= 12288) f(integral_constant<int, 512>{}, integral_constant<int, 3>{});
+    else if (K <= 16384) f(integral_constant<int, 512>{}, integral_constant<int, 4>{});
     else f(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
 }
 
