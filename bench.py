@@ -24,6 +24,7 @@ sample of the same workload.
     python bench.py --decode-set   # 7B-class decode step (224 products, B=32), table only
     python bench.py --kv           # decode attention over an int4 KV cache, table only
     python bench.py --kv-paged     # decode step over a paged int4 KV cache: rope, append, attention, table only
+    python bench.py --w8a8         # a 7B-class layer's 8-bit path at 1, 64 and 2048 tokens, table only
     python bench.py --ceiling      # load-only probe read rates (and plain torch rates), table only
 """
 
@@ -62,6 +63,9 @@ def parse():
                    help="decode step of one layer's attention over a paged int4 KV cache: rotary "
                         "positions, append and attention of 64 sequences of about 4096 tokens, "
                         "8 KV heads, 32 query heads (table line)")
+    p.add_argument("--w8a8", action="store_true",
+                   help="a 7B-class layer's 8-bit path (norms, quantizations and the four products, attention "
+                        "left out) at --batches tokens, default 1,64,2048 (table lines)")
     p.add_argument("--format", choices=["nf4", "offset"], default=None,
                    help="another weight format on the step's workload: NF4 at blocks of 64, or "
                         "the float-offset variant at the workload's group and --bits; quantize + "
@@ -873,6 +877,103 @@ def run_kv_paged(args, shape=KV_PAGED_SHAPE, layers=4):
     return row
 
 
+W8A8_SHAPE = (4096, 11008)           # width, feed-forward width
+
+
+def run_w8a8(args, shape=W8A8_SHAPE, layers=3):
+    """One layer's 8-bit path, its attention left out: norm to codes, q/k/v
+    product, codes of the attention's output (the q part stands for it), output
+    product, norm with the residual to codes, gate and up product, gated codes,
+    down product.  The weights of `layers` layers take turns (600 MB, beyond the
+    256 MB Infinity Cache).  The step is captured and replayed, so what counts
+    is the GPU's time; the kernels' own times are of eager bursts."""
+    import torch
+
+    import bit_weight_only_wq_amd as wq
+    from bit_weight_only_wq_amd import roofline as rl
+
+    K, F = shape
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    f16 = torch.float16
+
+    def weights(N, K):
+        return wq.quantize_rows(torch.randn((N, K), generator=gen, device="cuda").mul_(0.02).to(f16))
+
+    nets = [{"qkv": weights(3 * K, K), "o": weights(K, K), "gu": weights(2 * F, K), "down": weights(K, F)}
+            for _ in range(layers)]
+    norm = torch.ones(K, dtype=f16, device="cuda")
+    rows = []
+    for B in ([int(b) for b in args.batches.split(",")] if args.batches else [1, 64, 2048]):
+        x = torch.randn((B, K), generator=gen, device="cuda").to(f16)
+        stream = torch.randn((B, K), generator=gen, device="cuda").to(f16)
+        codes, scales = wq.quantize_rows(x)
+        wide, wide_scales = wq.quantize_rows(torch.randn((B, F), generator=gen, device="cuda").to(f16))
+        qkv, y = torch.empty((B, 3 * K), dtype=f16, device="cuda"), torch.empty((B, K), dtype=f16, device="cuda")
+        gu = torch.randn((B, 2 * F), generator=gen, device="cuda").to(f16)
+        ws = max((wq.gemm_w8a8_workspace(B, n, k) for n, k in ((3 * K, K), (K, K), (2 * F, K), (K, F))),
+                 key=lambda t: t.numel())
+        total = torch.empty_like(stream)
+        calls = {
+            "rmsnorm_quantize": (lambda i: wq.rmsnorm_quantize(x, norm, residual=stream, total=total, out=(codes, scales)),
+                                 7 * B * K + 2 * K + 4 * B, 0),
+            "gemm_qkv": (lambda i: wq.gemm_w8a8(codes, scales, *nets[i % layers]["qkv"], out=qkv, workspace=ws),
+                         rl.gemm_w8a8_bytes(B, 3 * K, K), 2 * B * 3 * K * K),
+            "quantize_rows": (lambda i: wq.quantize_rows(qkv[:, :K], out=(codes, scales)), 3 * B * K + 4 * B, 0),
+            "gemm_o": (lambda i: wq.gemm_w8a8(codes, scales, *nets[i % layers]["o"], out=y, workspace=ws),
+                       rl.gemm_w8a8_bytes(B, K, K), 2 * B * K * K),
+            "rmsnorm_quantize_2": (lambda i: wq.rmsnorm_quantize(y, norm, residual=total, total=total, out=(codes, scales)),
+                                   7 * B * K + 2 * K + 4 * B, 0),
+            "gemm_gate_up": (lambda i: wq.gemm_w8a8(codes, scales, *nets[i % layers]["gu"], out=gu, workspace=ws),
+                             rl.gemm_w8a8_bytes(B, 2 * F, K), 2 * B * 2 * F * K),
+            "quantize_rows_gated": (lambda i: wq.quantize_rows(gu[:, F:], gate=gu[:, :F], out=(wide, wide_scales)),
+                                    5 * B * F + 4 * B, 0),
+            "gemm_down": (lambda i: wq.gemm_w8a8(wide, wide_scales, *nets[i % layers]["down"], out=y, workspace=ws),
+                          rl.gemm_w8a8_bytes(B, K, F), 2 * B * K * F)}
+
+        def burst(fn, per):
+            for i in range(max(1, args.warmup)):
+                fn(i)
+            torch.cuda.synchronize()
+            e0 = torch.cuda.Event(enable_timing=True)
+            e1 = torch.cuda.Event(enable_timing=True)
+            e0.record()
+            for i in range(args.steps):
+                fn(i)
+            e1.record()
+            torch.cuda.synchronize()
+            return e0.elapsed_time(e1) / args.steps / per
+
+        for fn, _, _ in calls.values():
+            fn(0)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for i in range(layers):
+                for fn, _, _ in calls.values():
+                    fn(i)
+        ms = burst(lambda i: graph.replay(), layers)
+        kernels = {}
+        for name, (fn, nbytes, flops) in calls.items():
+            us = burst(fn, 1) * 1e3
+            kernels[name] = {"avg_us": round(us, 2), "achieved_GBps": round(nbytes / us / 1e3, 1),
+                             "achieved_TOPs": round(flops / us / 1e6, 1)}
+        nbytes = sum(c[1] for c in calls.values())
+        flops = sum(c[2] for c in calls.values())
+        bound = "hbm" if nbytes / rl.MI355X_HBM_BYTES_PER_S > flops / rl.MI355X_INT8_DENSE_OPS else "mfma"
+        got, peak, unit = ((nbytes / (ms * 1e-3) / 1e9, rl.MI355X_HBM_BYTES_PER_S / 1e9, "GB/s") if bound == "hbm" else
+                           (flops / (ms * 1e-3) / 1e12, rl.MI355X_INT8_DENSE_OPS / 1e12, "TOP/s"))
+        row = {"metric": f"a layer's 8-bit path: norms, quantizations, products ({unit})", "value": round(got, 1),
+               "unit": unit, "n_gpus": 1, "steps": args.steps, "warmup": args.warmup, "ms_per_step": round(ms, 4),
+               "higher_is_better": True, "dtype": "int8", "data": "synthetic",
+               "config": {"workload": "w8a8_layer", "tokens": B, "width": K, "ffn": F, "layers_in_turn": layers},
+               "roofline": {"bound": bound, "achieved": round(got, 1), "peak": round(peak, 1), "unit": unit,
+                            "frac": round(got / peak, 4), "bytes_per_step": int(nbytes), "ops_per_step": int(flops)},
+               "kernels": kernels}
+        print(json.dumps(row), flush=True)
+        rows.append(row)
+    return rows
+
+
 def run_format(args):
     """Another weight format on the step's workload: NF4 at blocks of 64 (the
     block the NF4 paragraph of "Gör inference billig" uses), or the
@@ -971,6 +1072,9 @@ def main():
         return
     if args.kv_paged:
         run_kv_paged(args)
+        return
+    if args.w8a8:
+        run_w8a8(args)
         return
     if args.format:
         run_format(args)

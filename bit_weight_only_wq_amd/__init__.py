@@ -496,25 +496,27 @@ def _vector(t, dtype, n, name, device):
     _line(t, dtype, n, name, device)
 
 
-def _apart(a, b, names):
-    """Refuses tensors (of 1 or 2 dimensions, rows contiguous) that share memory.
-    Rows of one stride that lie side by side are apart."""
-    if not a.numel() or not b.numel():
-        return
-    def shape(t):
-        n, st = (t.shape[0], t.stride(0)) if t.dim() == 2 else (1, 0)
-        return t.data_ptr(), n, st * t.element_size(), t.shape[-1] * t.element_size()
-    (pa, na, sa, ra), (pb, nb, sb, rb) = shape(a), shape(b)
-    d = pb - pa
-    if d >= (na - 1) * sa + ra or -d >= (nb - 1) * sb + rb:
-        return
-    if na > 1 and nb > 1 and sa == sb and ra <= d % sa <= sa - rb:
-        return
-    raise ValueError(f"{names[0]} overlaps {names[1]}")
+def _span(t):
+    """(first byte, end) of a tensor of 1 or 2 dimensions with contiguous rows."""
+    p, shape = t.data_ptr(), t.shape
+    n = shape[-1] if len(shape) == 1 or shape[0] <= 1 else (shape[0] - 1) * t.stride(0) + shape[1]
+    return p, p + n * t.element_size() if 0 not in shape else p
+
+
+def _apart(outs, ins):
+    """Refuses outputs that share memory with an input or another output: lists of
+    (tensor, name, span).  Rows of one stride that lie side by side are apart."""
+    for i, (a, name, (a0, a1)) in enumerate(outs):
+        for b, other, (b0, b1) in outs[i + 1:] + ins:
+            if a0 < b1 and b0 < a1:
+                sa, sb = (t.stride(0) * t.element_size() if t.dim() == 2 and t.shape[0] > 1 else 0 for t in (a, b))
+                ra, rb = (t.shape[-1] * t.element_size() for t in (a, b))
+                if sa != sb or sa == 0 or not ra <= (b0 - a0) % sa <= sa - rb:
+                    raise ValueError(f"{name} overlaps {other}")
 
 
 def _codes_out(out, x, rows, K, device, inputs):
-    """(codes, scales, stride) of a call: new, or the caller's."""
+    """(codes, scales, stride) of a call: new, or the caller's (inputs: as _apart's)."""
     import torch
     if out is None:
         # (like x: rows that are apart give contiguous ones)
@@ -522,11 +524,8 @@ def _codes_out(out, x, rows, K, device, inputs):
     codes, scales = out
     stride = _rows2(codes, torch.int8, rows, K, "codes", device)
     _vector(scales, torch.float32, rows, "scales", device)
-    _apart(codes, scales, ("codes", "scales"))
-    for t, name in inputs:
-        if t is not None:
-            _apart(codes, t, ("codes", name))
-            _apart(scales, t, ("scales", name))
+    _apart([(codes, "codes", _span(codes)), (scales, "scales", _span(scales))],
+           [(t, name, _span(t)) for t, name in inputs if t is not None])
     return codes, scales, stride
 
 
@@ -570,10 +569,10 @@ def _norm_inputs(x, weight, residual, total):
         ts = K
     else:
         ts = _rows2(total, dt, rows, K, "total", dev)
-        _apart(total, weight, ("total", "weight"))
-        for t, st, name in ((x, xs, "x"), (residual, rs, "residual")):
-            if not (total.data_ptr() == t.data_ptr() and ts == st):
-                _apart(total, t, ("total", name))
+        at = total.data_ptr()
+        _apart([(total, "total", _span(total))],
+               [(t, name, _span(t)) for t, st, name in ((x, xs, "x"), (residual, rs, "residual"), (weight, None, "weight"))
+                if not (at == t.data_ptr() and ts == st)])
     return code, rows, K, xs, residual.data_ptr(), rs, total, total.data_ptr(), ts
 
 
@@ -603,9 +602,8 @@ def rmsnorm(x, weight, residual=None, eps: float = 1e-6, total=None, out=None):
         os_ = K
     else:
         os_ = _rows2(out, x.dtype, rows, K, "out", dev)
-        for t, name in ((x, "x"), (weight, "weight"), (residual, "residual"), (total, "total")):
-            if t is not None:
-                _apart(out, t, ("out", name))
+        _apart([(out, "out", _span(out))], [(t, name, _span(t)) for t, name in (
+            (x, "x"), (weight, "weight"), (residual, "residual"), (total, "total")) if t is not None])
     _launch("wq_rmsnorm", dev, load().wq_rmsnorm, x.data_ptr(), xs, rp, rs, weight.data_ptr(), rows, K, code, eps, tp, ts,
             out.data_ptr(), os_)
     return out, total
@@ -614,10 +612,17 @@ def rmsnorm(x, weight, residual=None, eps: float = 1e-6, total=None, out=None):
 def gemm_w8a8_workspace(B: int, N: int, K: int, device="cuda"):
     """A workspace tensor for gemm_w8a8 calls of this shape that do not overlap
     (uint8, possibly empty)."""
+    import ctypes
     import torch
-    with torch.cuda.device(device):
-        need = _size_t(load().wq_gemm_w8a8_workspace_size, B, K, N, where="wq_gemm_w8a8")
-    return torch.empty(need, dtype=torch.uint8, device=device)
+    device = torch.device(device)
+    n = ctypes.c_size_t(0)
+    if device.index is None or torch.cuda.current_device() == device.index:
+        st = load().wq_gemm_w8a8_workspace_size(B, K, N, ctypes.byref(n))
+    else:
+        with torch.cuda.device(device):
+            st = load().wq_gemm_w8a8_workspace_size(B, K, N, ctypes.byref(n))
+    check(st, "wq_gemm_w8a8")
+    return torch.empty(n.value, dtype=torch.uint8, device=device)
 
 
 def gemm_w8a8(a, a_scales, w, w_scales, bias=None, dtype=None, out=None, workspace=None, use_workspace=True):
@@ -629,8 +634,8 @@ def gemm_w8a8(a, a_scales, w, w_scales, bias=None, dtype=None, out=None, workspa
     the batch and the workspace.  The workspace comes from torch or from
     `workspace` (gemm_w8a8_workspace); use_workspace=False does without."""
     import torch
-    if not isinstance(a, torch.Tensor) or a.dim() != 2 or not isinstance(w, torch.Tensor) or w.dim() != 2:
-        raise ValueError("a must be int8 [B, K] and w int8 [N, K]")
+    if not isinstance(a, torch.Tensor) or a.dim() != 2 or not isinstance(w, torch.Tensor) or w.dim() != 2 or not a.is_cuda:
+        raise ValueError("a must be int8 [B, K] and w int8 [N, K], GPU tensors")
     B, K = a.shape
     N = w.shape[0]
     dev = a.device
@@ -649,9 +654,8 @@ def gemm_w8a8(a, a_scales, w, w_scales, bias=None, dtype=None, out=None, workspa
         ys = N
     else:
         ys = _rows2(out, dtype, B, N, "out", dev)
-        for t, name in ((a, "a"), (w, "w"), (a_scales, "a_scales"), (w_scales, "w_scales"), (bias, "bias")):
-            if t is not None:
-                _apart(out, t, ("out", name))
+        _apart([(out, "out", _span(out))], [(t, name, _span(t)) for t, name in (
+            (a, "a"), (w, "w"), (a_scales, "a_scales"), (w_scales, "w_scales"), (bias, "bias")) if t is not None])
     if workspace is None and use_workspace:
         workspace = gemm_w8a8_workspace(B, N, K, dev)
     wp, wn = _given(workspace, dev) if workspace is not None and use_workspace else (None, 0)

@@ -14,6 +14,7 @@ from __future__ import annotations
 # MI355X published peaks (dense, no sparsity).
 MI355X_HBM_BYTES_PER_S = 8.0e12
 MI355X_FP16_MFMA_FLOPS = 2.5e15
+MI355X_INT8_DENSE_OPS = 5.0e15
 MI355X_FP32_VALU_FLOPS = 157.3e12
 MI355X_COMPUTE_UNITS = 256
 MI355X_CLOCK_HZ = 2.4e9
@@ -120,3 +121,9 @@ def kv_paged_append_bytes(heads: int, tokens: int, done: float) -> float:
     of the `done` blocks that become whole, the windows' other tokens read and a
     record written."""
     return heads * (tokens * 4 * 256 + done * (127 * 512 + 17408))
+
+
+def gemm_w8a8_bytes(B: int, N: int, K: int) -> int:
+    """One product of 8-bit activations and weights: both read once with their fp32
+    scales, the 16-bit result written."""
+    return B * K + N * K + 4 * (B + N) + 2 * B * N

@@ -185,7 +185,7 @@ def test_empty_and_refused():
                 lambda: wq.gemm_w8a8(a, sa, w, sw, bias=sw.half(), dtype=torch.bfloat16),
                 lambda: wq.gemm_w8a8(a, sa, w, sw, workspace=torch.zeros(64, device=dev)),
                 lambda: wq.gemm_w8a8(buf.view(i8)[:, :64], sa, w, sw, out=buf[:, :32]),
-                lambda: wq.gemm_w8a8(a, sa.cpu(), w, sw)]:
+                lambda: wq.gemm_w8a8(a, sa.cpu(), w, sw), lambda: wq.gemm_w8a8(a.cpu(), sa.cpu(), w.cpu(), sw.cpu())]:
         with pytest.raises(ValueError):
             bad()
     for bad in [lambda: wq.gemm_w8a8(a[:, :40], sa, w[:, :40], sw),              # K no multiple of 16

@@ -100,3 +100,16 @@ def test_layer(B):
     assert logits.shape == (B, vocab) and torch.isfinite(logits).all()
     a, sa, _ = wq.rmsnorm_quantize(y, n3, residual=stream)
     check_product(wq.gemm_w8a8(a, sa, *wv), a, sa, wv)
+
+
+def test_bench_line():
+    """bench.py's 8-bit table on a small layer."""
+    import types
+
+    import bench
+    device()
+    note("8-bit bench lines")
+    rows = bench.run_w8a8(types.SimpleNamespace(batches="1,33", steps=3, warmup=1), shape=(512, 1408), layers=2)
+    assert [r["config"]["tokens"] for r in rows] == [1, 33]
+    for r in rows:
+        assert r["value"] > 0 and r["roofline"]["bytes_per_step"] > 0 and len(r["kernels"]) == 8

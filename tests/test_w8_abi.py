@@ -109,3 +109,19 @@ def test_oracle_borders():
     y = w8_util.product(a, np.array([0.5], np.float32), np.array([[2, 127]], np.int8), np.array([0.25], np.float32),
                         torch.tensor([0.75]).half(), torch.float16)
     assert y.tolist() == [[(2 - 128 * 127) * 0.125 + 0.75]]
+
+
+def test_product_bytes():
+    from bit_weight_only_wq_amd import roofline as rl
+    assert rl.gemm_w8a8_bytes(3, 5, 16) == 48 + 80 + 4 * 8 + 30
+
+
+def test_cpu_tensors_are_refused():
+    """The binding never hands host memory to a kernel."""
+    h, i8 = torch.ones((4, 64)).half(), torch.ones((4, 64), dtype=torch.int8)
+    one = torch.ones(4)
+    for bad in [lambda: wq.quantize_rows(h), lambda: wq.rmsnorm(h, h[0]), lambda: wq.rmsnorm_quantize(h, h[0], residual=h),
+                lambda: wq.gemm_w8a8(i8, one, i8, one), lambda: wq.gemm_w8a8(i8, one, i8, one, out=h[:, :4]),
+                lambda: wq.quantize_rows(h.numpy()), lambda: wq.gemm_w8a8(None, one, i8, one)]:
+        with pytest.raises(ValueError):
+            bad()
