@@ -79,7 +79,9 @@ struct Spread {
 // Scales a wave's sums and stores them.  A lane holds, of every 32 x 32 block
 // (i, j), rows 8 (e / 4) + 4 (lane / 32) + e % 4 of A and column NF (lane % 32) + j
 // of the wave's W rows, so it has NF neighbouring values of a row of Y.  Y goes
-// through a buffer that ends with the last row: rows past it are dropped.
+// through a buffer that ends with the last row: rows past it are dropped.  The
+// stores are marked as streamed (the 2), so that Y does not push A and W out of the
+// caches: 8192 x 4096 x 22016 656 -> 618 us, 2048 x 4096 x 12288 122 -> 116.
 template <int MF, int NF, bool BF16>
 __device__ __forceinline__ bool w8_store(const W8Call& C, const i16_t (&acc)[MF][NF], int64_t b0, int64_t n0,
                                          const float* sal, const float* swl) {
@@ -124,9 +126,9 @@ __device__ __forceinline__ bool w8_store(const W8Call& C, const i16_t (&acc)[MF]
                     const int to = (int)(n < N ? at : kFar);
                     if constexpr (NF == 4) {
                         typedef unsigned int v2_t __attribute__((ext_vector_type(2)));
-                        __builtin_amdgcn_raw_buffer_store_b64(v2_t{o[0] | (uint32_t)o[1] << 16, o[2] | (uint32_t)o[3] << 16}, ry, to, 0, 0);
+                        __builtin_amdgcn_raw_buffer_store_b64(v2_t{o[0] | (uint32_t)o[1] << 16, o[2] | (uint32_t)o[3] << 16}, ry, to, 0, 2);
                     } else {
-                        __builtin_amdgcn_raw_buffer_store_b32(o[0] | (uint32_t)o[1] << 16, ry, to, 0, 0);
+                        __builtin_amdgcn_raw_buffer_store_b32(o[0] | (uint32_t)o[1] << 16, ry, to, 0, 2);
                     }
                 } else {
 #pragma unroll
