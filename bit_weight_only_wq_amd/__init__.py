@@ -7,6 +7,12 @@ library is not built, the calls raise.
 
     codes, scales, zeros = quantize_pack(W, group=128, bits=4)   # W fp16 [N, K] on the GPU
     Y = gemm(X, codes, scales, zeros, N=N, K=K, group=128, bits=4)  # X fp16 [B, K]
+
+and in 8 bits on both sides, for prompts and large batches:
+
+    w, w_scales = quantize_rows(W)                                # once
+    a, a_scales, h = rmsnorm_quantize(x, weight, residual=h, total=h)
+    Y = gemm_w8a8(a, a_scales, w, w_scales)
 """
 
 from __future__ import annotations

@@ -152,7 +152,7 @@ struct W8Tile {
 // meet, the slot is free and the other one has landed; in the second half the
 // slot is loaded anew and the next step's first operands are read.  So one meeting
 // a step, with products waiting on both sides of it.  8192 x 8192 x 28672: 1.51 ms,
-// 2550 TOP/s, of which the products' own time is 71 % of the cycles; the clock then
+// 2550 TOP/s; the products' own time is 73 % of the cycles, and the clock then
 // stands at 1.7 GHz, held there by power (operands of zeros: 1.37 ms).  Measured
 // besides: steps of 64 k in four slots 1.61 ms (twice the meetings, pieces of 64
 // bytes); four waves of 128 x 128 1.59 ms; workgroups that end with their tile
