@@ -470,29 +470,55 @@ void run_rows_vec(const RowsCall& c, hipStream_t stream) {
 
 }  // namespace
 
-constexpr int64_t kWidest = 32768;   // values of a row that 1024 threads hold
+constexpr int64_t kWidest = 32768;          // values of a row that 1024 threads hold
+constexpr int64_t kRows = (int64_t)1 << 20;   // of a launch: a grid holds fewer than 2^32 threads
 
-hipError_t launch_norm(const NormCall& c, hipStream_t stream) {
-    const bool vec = c.K % 8 == 0 && c.K <= kWidest && by(c.x, c.x_stride, 16, 2) && by(c.residual, c.residual_stride, 16, 2) &&
-                     by(c.weight, 0, 16, 2) && by(c.total, c.total_stride, 16, 2) && by(c.codes, c.codes_stride, 8, 1) &&
-                     by(c.out, c.out_stride, 16, 2);
-    if (!vec) norm_any_kernel<<<dim3((unsigned)c.rows), dim3(kThreads), 0, stream>>>(c);
-    else if (c.codes && c.bf16) run_norm_vec<MODE_NORM_CODES, true>(c, stream);
-    else if (c.codes) run_norm_vec<MODE_NORM_CODES, false>(c, stream);
-    else if (c.bf16) run_norm_vec<MODE_NORM_VALUES, true>(c, stream);
-    else run_norm_vec<MODE_NORM_VALUES, false>(c, stream);
-    return hipGetLastError();
+static const void* after(const void* p, int64_t bytes) { return p ? static_cast<const char*>(p) + bytes : nullptr; }
+static void* after(void* p, int64_t bytes) { return p ? static_cast<char*>(p) + bytes : nullptr; }
+
+hipError_t launch_norm(const NormCall& all, hipStream_t stream) {
+    for (int64_t r = 0; r < all.rows; r += kRows) {
+        NormCall c = all;
+        c.rows = all.rows - r < kRows ? all.rows - r : kRows;
+        c.x = after(all.x, 2 * r * all.x_stride);
+        c.residual = after(all.residual, 2 * r * all.residual_stride);
+        c.total = after(all.total, 2 * r * all.total_stride);
+        c.codes = after(all.codes, r * all.codes_stride);
+        c.out = after(all.out, 2 * r * all.out_stride);
+        c.scales = all.scales ? all.scales + r : nullptr;
+        const bool vec = c.K % 8 == 0 && c.K <= kWidest && by(c.x, c.x_stride, 16, 2) && by(c.residual, c.residual_stride, 16, 2) &&
+                         by(c.weight, 0, 16, 2) && by(c.total, c.total_stride, 16, 2) && by(c.codes, c.codes_stride, 8, 1) &&
+                         by(c.out, c.out_stride, 16, 2);
+        if (!vec) norm_any_kernel<<<dim3((unsigned)c.rows), dim3(kThreads), 0, stream>>>(c);
+        else if (c.codes && c.bf16) run_norm_vec<MODE_NORM_CODES, true>(c, stream);
+        else if (c.codes) run_norm_vec<MODE_NORM_CODES, false>(c, stream);
+        else if (c.bf16) run_norm_vec<MODE_NORM_VALUES, true>(c, stream);
+        else run_norm_vec<MODE_NORM_VALUES, false>(c, stream);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
-hipError_t launch_rows(const RowsCall& c, hipStream_t stream) {
-    const bool vec = c.K % 8 == 0 && c.K <= kWidest && by(c.x, c.x_stride, 16, 2) && by(c.gate, c.gate_stride, 16, 2) &&
-                     by(c.codes, c.codes_stride, 8, 1);
-    if (!vec) rows_any_kernel<<<dim3((unsigned)c.rows), dim3(kThreads), 0, stream>>>(c);
-    else if (c.gate && c.bf16) run_rows_vec<MODE_GATED, true>(c, stream);
-    else if (c.gate) run_rows_vec<MODE_GATED, false>(c, stream);
-    else if (c.bf16) run_rows_vec<MODE_ROWS, true>(c, stream);
-    else run_rows_vec<MODE_ROWS, false>(c, stream);
-    return hipGetLastError();
+hipError_t launch_rows(const RowsCall& all, hipStream_t stream) {
+    for (int64_t r = 0; r < all.rows; r += kRows) {
+        RowsCall c = all;
+        c.rows = all.rows - r < kRows ? all.rows - r : kRows;
+        c.x = after(all.x, 2 * r * all.x_stride);
+        c.gate = after(all.gate, 2 * r * all.gate_stride);
+        c.codes = after(all.codes, r * all.codes_stride);
+        c.scales = all.scales + r;
+        const bool vec = c.K % 8 == 0 && c.K <= kWidest && by(c.x, c.x_stride, 16, 2) && by(c.gate, c.gate_stride, 16, 2) &&
+                         by(c.codes, c.codes_stride, 8, 1);
+        if (!vec) rows_any_kernel<<<dim3((unsigned)c.rows), dim3(kThreads), 0, stream>>>(c);
+        else if (c.gate && c.bf16) run_rows_vec<MODE_GATED, true>(c, stream);
+        else if (c.gate) run_rows_vec<MODE_GATED, false>(c, stream);
+        else if (c.bf16) run_rows_vec<MODE_ROWS, true>(c, stream);
+        else run_rows_vec<MODE_ROWS, false>(c, stream);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace wq

@@ -254,6 +254,30 @@ def test_large_norm_sums():
     check_values(v, y, torch.bfloat16, "values")
 
 
+@pytest.mark.parametrize("K,pad", [(8, 0), (5, 3), (520, 0)])
+def test_more_rows_than_a_launch(K, pad):
+    """Rows on both sides of 2^20, where a second launch takes over, 16-byte form
+    and not."""
+    dev = device()
+    R = (1 << 20) + 5
+    note(f"many rows K={K}")
+    g = torch.Generator(device=dev).manual_seed(K)
+    x = torch.randn((R, K + pad), generator=g, device=dev).half()[:, :K]
+    gate = torch.randn((R, K), generator=g, device=dev).half()
+    w = torch.ones(K, dtype=torch.float16, device=dev)
+    codes, scales = wq.quantize_rows(x, gate=gate)
+    c, s, total = wq.rmsnorm_quantize(x, w, residual=gate)
+    y, _ = wq.rmsnorm(x, w)
+    for lo in (0, (1 << 20) - 4):
+        part = slice(lo, lo + 9)
+        hx, hg = x[part].cpu(), gate[part].cpu()
+        check_codes(codes[part], scales[part], *w8_util.rows(hx, hg), 2.0 ** -22, "gated")
+        _, want, ws, h = w8_util.norm(hx, w.cpu(), hg, 1e-6)
+        check_codes(c[part], s[part], want, ws, 2.0 ** -21, "norm")
+        assert torch.equal(bits(total[part]), bits(h))
+        check_values(y[part], w8_util.norm(hx, w.cpu(), None, 1e-6)[0], torch.float16, "values")
+
+
 def test_empty_and_refused():
     dev = device()
     f16 = torch.float16
