@@ -327,25 +327,29 @@ __global__ __launch_bounds__(THREADS, 1) void w8_wide_kernel(const W8Call C, int
 }
 
 // A workgroup's tile of BM rows of A and BN rows of W through a ring of S slots of
-// 128 k, loaded S - 1 steps ahead; a wave takes WM by WN of it.  With splits, part z
+// 128 k, loaded S - 1 steps ahead; a wave takes WM by WN of it.  KG groups of waves
+// take parts of K, each with a ring of its own, and meet at the end: where there is
+// one workgroup a compute unit, a step's own latency (meeting, reads from LDS,
+// products one after another) is what counts, and KG steps then run at once.  With splits, part z
 // of K goes to plane z of the partial sums.  28672 x 8192: 42 us at one row, 43 at
 // 16 (5.5 TB/s; a kernel that only reads gets 6.5), 47 at 64, 59 at 128.  W straight
 // to registers instead, K split over a workgroup's waves, took 49 us at one row and
 // 72 at 16 (pieces of 64 bytes, A read by every wave); lines of W asked for into the
 // cache further ahead made it slower (42 -> 65 us), and so did no shift of the walks
 // (45 -> 49 us at one row).
-template <int BM, int BN, int WM, int WN, int S, int THREADS = (BM / WM) * (BN / WN) * 64>
+template <int BM, int BN, int WM, int WN, int S, int KG, int THREADS = KG * (BM / WM) * (BN / WN) * 64>
 __global__ __launch_bounds__(THREADS) void w8_ring_kernel(const W8Call C, int* part, int splits, int split_steps) {
-    constexpr int WAVES = THREADS / 64, MF = WM / 16, NF = WN / 16;
+    constexpr int WAVES = THREADS / 64 / KG, MF = WM / 16, NF = WN / 16;   // (waves of a group)
     constexpr int RM = BM < 8 * WAVES ? 8 * WAVES : BM;             // rows of a slot: whole loads for every wave
     constexpr int LA = RM / 8 / WAVES, LW = BN / 8 / WAVES;
     static_assert(RM % (8 * WAVES) == 0 && BN % (8 * WAVES) == 0, "loads divide evenly");
     constexpr int SLOT = (RM + BN) * 8;
-    __shared__ __align__(1024) uint4 s0[SLOT], s1[SLOT], s2[SLOT], s3[SLOT];
-    constexpr int MORE = S == 8 ? SLOT : 1;
+    __shared__ __align__(1024) uint4 s0[KG * SLOT], s1[KG * SLOT], s2[KG * SLOT], s3[KG * SLOT];
+    constexpr int MORE = S == 8 ? KG * SLOT : 1;
     __shared__ __align__(1024) uint4 s4[MORE], s5[MORE], s6[MORE], s7[MORE];
     static_assert(S == 4 || S == 8, "the walk below");
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, any_wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = any_wave % WAVES, group = any_wave / WAVES;
     const int wm = wave % (BM / WM), wn = wave / (BM / WM);
     const int r16 = lane & 15, g4 = lane >> 4;
     // The eight XCDs take runs of the order rows of A, then of W, then splits of K:
@@ -359,11 +363,13 @@ __global__ __launch_bounds__(THREADS) void w8_ring_kernel(const W8Call C, int* p
     const uint8_t* const a = static_cast<const uint8_t*>(C.A) + b0 * C.a_stride;
     const uint8_t* const w = static_cast<const uint8_t*>(C.W) + n0 * C.w_stride;
     const uint32_t K = (uint32_t)C.K;
-    const int first = z * split_steps, all = (int)((K + kStep - 1) / kStep);
-    const int steps = all - first < split_steps ? all - first : split_steps;
+    // This workgroup's part of K, and this group's part of that (which may be empty).
+    const int all = (int)((K + kStep - 1) / kStep) - z * split_steps, part_steps = all < split_steps ? all : split_steps;
+    const int turns = (part_steps + KG - 1) / KG, first = z * split_steps + group * turns;
+    const int left = part_steps - group * turns, steps = left < turns ? (left > 0 ? left : 0) : turns;
     // Workgroups start their walks over K at different steps (and wrap): rows lie
     // K apart, and the same columns of many rows fall on the same memory channels.
-    const int shift = (id / tiles_m) * 5 % steps;
+    const int shift = steps > 0 ? (id / tiles_m) * 5 % steps : 0;
     const uint32_t abytes = (uint32_t)(rows_a - 1) * (uint32_t)C.a_stride + K;
     const uint32_t wbytes = (uint32_t)(rows_w - 1) * (uint32_t)C.w_stride + K;
     // Chunk c of row p lies at c ^ (p / 2 & 7).
@@ -384,11 +390,11 @@ __global__ __launch_bounds__(THREADS) void w8_ring_kernel(const W8Call C, int* p
         const bool in = k + chunk < (step < steps ? K : 0u);
 #pragma unroll
         for (int q = 0; q < LW; ++q)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (w8_lds_t*)(s + 64 * (WAVES * q + wave)), 16,
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (w8_lds_t*)(s + group * SLOT + 64 * (WAVES * q + wave)), 16,
                                                      (int)(in ? woff[q] : kFar), (int)k, 0, 0);
 #pragma unroll
         for (int q = 0; q < LA; ++q)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (w8_lds_t*)(s + BN * 8 + 64 * (WAVES * q + wave)), 16,
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (w8_lds_t*)(s + group * SLOT + BN * 8 + 64 * (WAVES * q + wave)), 16,
                                                      (int)(in ? aoff[q] : kFar), (int)k, 0, 0);
     };
     i4_t acc[MF][NF];
@@ -401,13 +407,14 @@ __global__ __launch_bounds__(THREADS) void w8_ring_kernel(const W8Call C, int* p
         i4_t a[2][MF], w[2][NF];
     };
     const int c0 = g4 ^ key, c1 = (4 + g4) ^ key;
+    const int wrow = group * SLOT + (wn * WN + r16) * 8, arow = group * SLOT + BN * 8 + (wm * WM + r16) * 8;
     const auto read = [&](Frags& f, const uint4* s) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
-            for (int j = 0; j < NF; ++j) f.w[h][j] = __builtin_bit_cast(i4_t, s[(wn * WN + j * 16 + r16) * 8 + (h ? c1 : c0)]);
+            for (int j = 0; j < NF; ++j) f.w[h][j] = __builtin_bit_cast(i4_t, s[wrow + j * 128 + (h ? c1 : c0)]);
 #pragma unroll
-            for (int m = 0; m < MF; ++m) f.a[h][m] = __builtin_bit_cast(i4_t, s[BN * 8 + (wm * WM + m * 16 + r16) * 8 + (h ? c1 : c0)]);
+            for (int m = 0; m < MF; ++m) f.a[h][m] = __builtin_bit_cast(i4_t, s[arow + m * 128 + (h ? c1 : c0)]);
         }
     };
     const auto mm = [&](const Frags& f) {
@@ -439,14 +446,14 @@ __global__ __launch_bounds__(THREADS) void w8_ring_kernel(const W8Call C, int* p
         read(g, next);
         mm(f);
     };
-    for (int u = 0; u < steps; u += S) {
+    for (int u = 0; u < turns; u += S) {
         one(u, s0, s1, f0, f1);
         one(u + 1, s1, s2, f1, f0);
         one(u + 2, s2, s3, f0, f1);
         if constexpr (S == 4) one(u + 3, s3, s0, f1, f0);
         if constexpr (S == 8) {
             one(u + 3, s3, s4, f1, f0);
-            if (u + 4 >= steps) break;
+            if (u + 4 >= turns) break;
             one(u + 4, s4, s5, f0, f1);
             one(u + 5, s5, s6, f1, f0);
             one(u + 6, s6, s7, f0, f1);
@@ -454,6 +461,26 @@ __global__ __launch_bounds__(THREADS) void w8_ring_kernel(const W8Call C, int* p
         }
     }
     __builtin_amdgcn_s_waitcnt(0);
+    if constexpr (KG > 1) {
+        // The groups' sums meet in the first group's registers.
+        constexpr int EACH = MF * NF * 64 * WAVES;
+        static_assert((KG - 1) * EACH <= KG * SLOT, "the sums fit a slot");
+        i4_t* const sums = reinterpret_cast<i4_t*>(s0);
+        w8_meet();
+        if (group > 0)
+#pragma unroll
+            for (int m = 0; m < MF; ++m)
+#pragma unroll
+                for (int j = 0; j < NF; ++j) sums[(group - 1) * EACH + ((m * NF + j) * WAVES + wave) * 64 + lane] = acc[m][j];
+        __syncthreads();
+        if (group > 0) return;
+#pragma unroll
+        for (int g = 0; g < KG - 1; ++g)
+#pragma unroll
+            for (int m = 0; m < MF; ++m)
+#pragma unroll
+                for (int j = 0; j < NF; ++j) acc[m][j] += sums[g * EACH + ((m * NF + j) * WAVES + wave) * 64 + lane];
+    }
 
     // A lane holds four neighbouring columns of row r16 of each block.
     const uint16_t* bias = static_cast<const uint16_t*>(C.bias);
@@ -544,12 +571,13 @@ constexpr W8Cost kCosts[] = {
 int64_t w8_ceil(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Up to 64 rows what counts is that all of the GPU reads W: the widest tile that
-// still gives about one workgroup a compute unit.  One row of 8192 x 4096 (K x N):
-// 32 rows of W a workgroup, 11 x 4096: 7 us, 64: 8.5, 128: 11; of 28672 x 8192 (N x K)
-// 128: 42 us, 64: 44, 32: 46.  K is split where that leaves compute units idle: 1024
-// x 8192 in four parts 7.7 us, in one 11; 4096 x 4096 in two 7.9, in one 6.9 (a part
-// keeps 16 steps).  Past 64 rows the least of the costs above: 333 x 11008 x 4096 takes
-// 128 x 128 in two parts, 33 us (128 x 64 in one: 35; 64 x 64: 39; 256 x 256: 108).
+// still gives about one workgroup a compute unit.  One row, N = 4096, K = 4096: 32 rows
+// of W a workgroup 7 us, 64: 8.5, 128: 11.  One row, N = 28672, K = 8192: 128 rows 42 us,
+// 64: 44, 32: 46.  K is split where that leaves compute units idle, into parts of 16
+// steps at least: N = 1024, K = 8192 in four parts 7.7 us, in one 11; N = 4096, K = 4096
+// in two 7.9, in one 6.9.  Past 64 rows the least of the costs above: B = 333, K =
+// 11008, N = 4096 takes 128 x 128 in two parts, 33 us (128 x 64 in one: 35; 64 x 64: 39;
+// 256 x 256: 108).
 W8Plan w8_plan(int64_t B, int64_t K, int64_t N, int cus, bool scratch) {
     const int64_t steps = w8_ceil(K, kStep);
     const auto parts = [&](int64_t tiles, int64_t room) {
@@ -590,7 +618,7 @@ W8Plan w8_plan(int64_t B, int64_t K, int64_t N, int cus, bool scratch) {
     return best;
 }
 
-template <int BM, int BN, int WM, int WN, int S>
+template <int BM, int BN, int WM, int WN, int S, int KG = 1>
 hipError_t run_ring(const W8Call& c, int splits, const Scratch& ws, hipStream_t stream) {
     const int64_t steps = w8_ceil(c.K, kStep);
     const int each = (int)(w8_ceil(w8_ceil(steps, splits), S) * S);
@@ -599,12 +627,24 @@ hipError_t run_ring(const W8Call& c, int splits, const Scratch& ws, hipStream_t 
     ws.want(splits > 1 ? (size_t)(16 * quads * c.B * splits) : 0);
     if (ws.sizing()) return hipSuccess;
     const int64_t tiles = w8_ceil(c.N, BN) * w8_ceil(c.B, BM);
-    w8_ring_kernel<BM, BN, WM, WN, S><<<dim3((unsigned)(tiles * splits)), dim3((BM / WM) * (BN / WN) * 64), 0, stream>>>(
+    w8_ring_kernel<BM, BN, WM, WN, S, KG><<<dim3((unsigned)(tiles * splits)), dim3(KG * (BM / WM) * (BN / WN) * 64), 0, stream>>>(
         c, static_cast<int*>(ws.ptr), splits, each);
     if (splits > 1)
         w8_join_kernel<<<dim3((unsigned)w8_ceil(quads * c.B, 256)), dim3(256), 0, stream>>>(c, static_cast<const int*>(ws.ptr),
                                                                                              splits);
     return hipGetLastError();
+}
+
+// Two groups of waves where there is about one workgroup a compute unit and each has
+// 16 steps or more: 1 x 4096 x 4096 7.1 -> 6.4 us, 1 x 11008 x 4096 15.4 -> 12.9,
+// 128 x 4096 x 4096 9.9 -> 9.1; with four steps (512 x 512) one group takes 3.9,
+// two 4.3, and with more workgroups than compute units neither gains.
+template <int BM, int BN, int WM, int WN, int S1, int S2>
+hipError_t run_ring_groups(const W8Call& c, int splits, int num_cus, const Scratch& ws, hipStream_t stream) {
+    const int64_t tiles = w8_ceil(c.N, BN) * w8_ceil(c.B, BM);
+    if (4 * tiles * splits <= 5 * (int64_t)num_cus && w8_ceil(c.K, kStep) >= 16 * (int64_t)splits)
+        return run_ring<BM, BN, WM, WN, S2, 2>(c, splits, ws, stream);
+    return run_ring<BM, BN, WM, WN, S1>(c, splits, ws, stream);
 }
 
 template <int BM, int BN, int WM, int WN>
@@ -622,12 +662,12 @@ hipError_t run_wide(const W8Call& c, int num_cus, const Scratch& ws, hipStream_t
 hipError_t launch_gemm_w8(const W8Call& c, int num_cus, const Scratch& ws, hipStream_t stream) {
     const W8Plan p = w8_plan(c.B, c.K, c.N, num_cus, ws.sizing() || ws.ptr);
     switch (p.shape) {
-        case R16x32: return run_ring<16, 32, 16, 16, 8>(c, p.splits, ws, stream);
-        case R32x32: return run_ring<32, 32, 16, 16, 8>(c, p.splits, ws, stream);
+        case R16x32: return run_ring_groups<16, 32, 16, 16, 8, 8>(c, p.splits, num_cus, ws, stream);
+        case R32x32: return run_ring_groups<32, 32, 16, 16, 8, 4>(c, p.splits, num_cus, ws, stream);
         case R32x64: return run_ring<32, 64, 32, 16, 4>(c, p.splits, ws, stream);
         case R32x128: return run_ring<32, 128, 32, 16, 4>(c, p.splits, ws, stream);
-        case R64x32: return run_ring<64, 32, 32, 16, 4>(c, p.splits, ws, stream);
-        case R64x64: return run_ring<64, 64, 32, 32, 4>(c, p.splits, ws, stream);
+        case R64x32: return run_ring_groups<64, 32, 32, 16, 4, 4>(c, p.splits, num_cus, ws, stream);
+        case R64x64: return run_ring_groups<64, 64, 32, 32, 4, 4>(c, p.splits, num_cus, ws, stream);
         case R64x128: return run_ring<64, 128, 32, 32, 4>(c, p.splits, ws, stream);
         case R128x64: return run_ring<128, 64, 32, 32, 4>(c, p.splits, ws, stream);
         case R128x128: return run_ring<128, 128, 64, 32, 4>(c, p.splits, ws, stream);

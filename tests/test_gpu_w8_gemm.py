@@ -63,7 +63,9 @@ def test_models_products(B, K, N, dt):
     (20, 304, 16500), (32, 512, 16640), (7, 1040, 9000), (60, 304, 16501), (49, 640, 9000), (40, 8192, 5200),
     (700, 8208, 3000), (500, 8208, 2050), (130, 4112, 8200), (1025, 272, 8200), (2300, 272, 8200), (2300, 96, 8200),
     (4300, 272, 8200), (4300, 112, 8195), (4300, 400, 8192), (300, 16, 20000), (20000, 16, 300), (20000, 144, 17),
-    (1100, 304, 2050), (2100, 1168, 2052), (600, 28672, 2050)])
+    (1100, 304, 2050), (2100, 1168, 2052), (600, 28672, 2050),
+    # (two groups of waves: parts of K that are not equally long)
+    (3, 2064, 3000), (16, 4240, 1030), (25, 2192, 2000), (50, 2320, 2000), (100, 2192, 1500), (200, 2320, 4100), (9, 6032, 700)])
 @pytest.mark.parametrize("dt,bias", [("fp16", False), ("bf16", True)])
 def test_many_tiles(B, K, N, dt, bias):
     device()
