@@ -344,23 +344,34 @@ def dequantize(codes, scales, zeros, N: int, K: int, group: int = 128, bits: int
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 
 
-def _raw_stream(index):
-    """Handle of the current stream of GPU `index`.  (torch's own call for it
-    costs 0.1 us, a Stream object 2.8 us: more than a launch.)"""
-    import torch
-    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return get(index) if get is not None else torch.cuda.current_stream(index).cuda_stream
+_torch_calls = None
+
+
+def _current():
+    """torch's calls for the current GPU's index and for the handle of the current
+    stream of a GPU.  (Its own C functions cost 0.1 us each, a Stream object 2.8 us:
+    more than a launch.)"""
+    global _torch_calls
+    if _torch_calls is None:
+        import torch
+        get = getattr(torch._C, "_cuda_getDevice", None)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        torch.cuda.current_device()                     # (initialises, once)
+        _torch_calls = (get or torch.cuda.current_device,
+                        raw or (lambda index: torch.cuda.current_stream(index).cuda_stream))
+    return _torch_calls
 
 
 def _launch(where, device, fn, *args):
     """fn(*args, stream) on `device` and its current stream."""
-    import torch
+    current, stream = _torch_calls or _current()
     index = device.index
-    if torch.cuda.current_device() == index:
-        st = fn(*args, _raw_stream(index))
+    if current() == index:
+        st = fn(*args, stream(index))
     else:
+        import torch
         with torch.cuda.device(device):
-            st = fn(*args, _raw_stream(index))
+            st = fn(*args, stream(index))
     if st:
         check(st, where)
 
