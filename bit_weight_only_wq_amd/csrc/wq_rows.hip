@@ -73,7 +73,7 @@ __device__ __forceinline__ float norm_factor(const NormCall& A, double sum) {
 
 __device__ __forceinline__ double silu64(double g) { return g / (1.0 + exp(-g)); }
 
-// One workgroup a row, one value at a time; any size, stride and alignment.
+// Rows past what registers hold: one workgroup a row, one value at a time.
 __global__ __launch_bounds__(kThreads) void norm_any_kernel(const NormCall A) {
     const int64_t row = blockIdx.x;
     const uint16_t* x = static_cast<const uint16_t*>(A.x) + row * A.x_stride;
@@ -141,7 +141,7 @@ __global__ __launch_bounds__(kThreads) void rows_any_kernel(const RowsCall A) {
     if (threadIdx.x == 0) A.scales[row] = bads ? __builtin_nanf("") : scale == 0.0f ? 1.0f : scale;
 }
 
-// ---- 16-byte form --------------------------------------------------------------
+// ---- rows in registers ----------------------------------------------------------
 //
 // TPR threads take a row of up to 8 TPR VPT values, kept in registers from the one
 // load to the codes; a wave takes a row by itself where it is short (no meeting),
@@ -150,6 +150,30 @@ __global__ __launch_bounds__(kThreads) void rows_any_kernel(const RowsCall A) {
 enum { MODE_NORM_CODES, MODE_NORM_VALUES, MODE_ROWS, MODE_GATED };
 
 typedef unsigned int u4_t __attribute__((ext_vector_type(4)));
+typedef unsigned int u2_t __attribute__((ext_vector_type(2)));
+// Global memory takes wide accesses at any address: norms of 8192 rows of 8192 values
+// 88 us, of 8191 133, one value at a time 255.
+typedef u4_t u4_any __attribute__((aligned(2)));
+typedef u2_t u2_any __attribute__((aligned(1)));
+
+// Eight values at p, of which the first n exist (n < 8 at a row's end only).
+__device__ __forceinline__ u4_t load8(const uint16_t* p, int n) {
+    if (n >= 8) return *reinterpret_cast<const u4_any*>(p);
+    u4_t v = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+        if (e < n) v[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
+    return v;
+}
+__device__ __forceinline__ void store8(uint16_t* p, u4_t v, int n) {
+    if (n >= 8) {
+        *reinterpret_cast<u4_any*>(p) = v;
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+        if (e < n) p[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+}
 
 template <bool BF16>
 __device__ __forceinline__ float part(u4_t v, int e) {
@@ -248,7 +272,7 @@ __device__ __forceinline__ uint2 codes8(const float (&t)[8], float inv, float wi
 // at place k of the row): vector by vector their waits add up (64 rows of 28672
 // gated values 12.7 instead of 11.6 us).
 template <int TPR, int VPT, class F>
-__device__ __forceinline__ void write_codes(const float (&t)[VPT][8], int8_t* codes, int nv, bool none, float top, double most,
+__device__ __forceinline__ void write_codes(const float (&t)[VPT][8], int8_t* codes, int K, bool none, float top, double most,
                                             float win, F value) {
     static_assert(VPT <= 4, "a bit for each value");
     const int tid = threadIdx.x % TPR;
@@ -258,12 +282,19 @@ __device__ __forceinline__ void write_codes(const float (&t)[VPT][8], int8_t* co
     uint32_t close = 0;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int v = i * TPR + tid;
-        if (v >= nv) continue;
+        const int k = 8 * (i * TPR + tid), n = K - k;
+        if (n <= 0) continue;
         uint32_t near = 0;
         uint2 c = make_uint2(0, 0);
         if (!none) c = codes8(t[i], inv, win, near);
-        reinterpret_cast<uint2*>(codes)[v] = c;
+        if (n >= 8) {
+            *reinterpret_cast<u2_any*>(codes + k) = u2_t{c.x, c.y};
+        } else {
+            near &= (1u << n) - 1;
+#pragma unroll
+            for (int e = 0; e < 7; ++e)
+                if (e < n) codes[k + e] = (int8_t)((e < 4 ? c.x : c.y) >> (8 * (e & 3)));
+        }
         close |= near << (8 * i);
     }
     while (close) {
@@ -281,21 +312,21 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_vec_kernel(const N
     __shared__ double sums[TPR / kWave];
     const int64_t row = (int64_t)blockIdx.x * RPB + (RPB > 1 ? threadIdx.x / TPR : 0);
     if (RPB > 1 && row >= A.rows) return;                           // (a whole wave)
-    const int tid = threadIdx.x % TPR, nv = (int)(A.K >> 3);
-    const u4_t* x = reinterpret_cast<const u4_t*>(static_cast<const uint16_t*>(A.x) + row * A.x_stride);
-    const u4_t* res = reinterpret_cast<const u4_t*>(static_cast<const uint16_t*>(A.residual) + row * A.residual_stride);
-    const u4_t* wt = static_cast<const u4_t*>(A.weight);
-    u4_t* total = reinterpret_cast<u4_t*>(static_cast<uint16_t*>(A.total) + row * A.total_stride);
+    const int tid = threadIdx.x % TPR, K = (int)A.K;
+    const uint16_t* x = static_cast<const uint16_t*>(A.x) + row * A.x_stride;
+    const uint16_t* res = static_cast<const uint16_t*>(A.residual) + row * A.residual_stride;
+    const uint16_t* wt = static_cast<const uint16_t*>(A.weight);
+    uint16_t* total = static_cast<uint16_t*>(A.total) + row * A.total_stride;
     const bool add = A.residual != nullptr;
     u4_t h[VPT], b[VPT], w[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int v = i * TPR + tid;
+        const int k = 8 * (i * TPR + tid), n = K - k;
         h[i] = b[i] = w[i] = u4_t{0, 0, 0, 0};
-        if (v < nv) {
-            h[i] = x[v];
-            if (add) b[i] = res[v];
-            w[i] = wt[v];
+        if (n > 0) {
+            h[i] = load8(x + k, n);
+            if (add) b[i] = load8(res + k, n);
+            w[i] = load8(wt + k, n);
         }
     }
     float t[VPT][8];
@@ -303,13 +334,13 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_vec_kernel(const N
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int v = i * TPR + tid;
+        const int k = 8 * (i * TPR + tid), n = K - k;
         if (add) {
             float f[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[e] = part<BF16>(h[i], e) + part<BF16>(b[i], e);
             h[i] = pack8<BF16>(f);
-            if (v < nv) total[v] = h[i];
+            if (n > 0) store8(total + k, h[i], n);
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -323,23 +354,23 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_vec_kernel(const N
     row_join<TPR>(top, sum, tops, sums);
     const float r = norm_factor(A, sum);
     if constexpr (MODE == MODE_NORM_VALUES) {
-        u4_t* out = reinterpret_cast<u4_t*>(static_cast<uint16_t*>(A.out) + row * A.out_stride);
+        uint16_t* out = static_cast<uint16_t*>(A.out) + row * A.out_stride;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int v = i * TPR + tid;
+            const int k = 8 * (i * TPR + tid), n = K - k;
             float f[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[e] = t[i][e] * r;
-            if (v < nv) out[v] = pack8<BF16>(f);
+            if (n > 0) store8(out + k, pack8<BF16>(f), n);
         }
         return;
     }
     const bool fine = top < kInfBits && sum < __builtin_inf();
     const float amax = __builtin_bit_cast(float, top);
-    const uint16_t* from = reinterpret_cast<const uint16_t*>(add ? total : x);
-    write_codes<TPR>(t, static_cast<int8_t*>(A.codes) + row * A.codes_stride, nv, !fine || !top, amax, (double)amax, 0x1p-14f,
+    const uint16_t* from = add ? total : x;
+    write_codes<TPR>(t, static_cast<int8_t*>(A.codes) + row * A.codes_stride, K, !fine || !top, amax, (double)amax, 0x1p-14f,
                      [&](int k) {
-                         return (double)(to_float(from[k], BF16) * to_float(static_cast<const uint16_t*>(A.weight)[k], BF16));
+                         return (double)(to_float(from[k], BF16) * to_float(wt[k], BF16));
                      });
     if (tid == 0) A.scales[row] = !fine ? __builtin_nanf("") : top ? r * amax / 127.0f : 1.0f;
 }
@@ -352,23 +383,23 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rows_vec_kernel(const R
     __shared__ double sums[TPR / kWave], mosts[TPR / kWave];
     const int64_t row = (int64_t)blockIdx.x * RPB + (RPB > 1 ? threadIdx.x / TPR : 0);
     if (RPB > 1 && row >= A.rows) return;                           // (a whole wave)
-    const int tid = threadIdx.x % TPR, nv = (int)(A.K >> 3);
-    const u4_t* x = reinterpret_cast<const u4_t*>(static_cast<const uint16_t*>(A.x) + row * A.x_stride);
-    const u4_t* g = reinterpret_cast<const u4_t*>(static_cast<const uint16_t*>(A.gate) + row * A.gate_stride);
+    const int tid = threadIdx.x % TPR, K = (int)A.K;
+    const uint16_t* x = static_cast<const uint16_t*>(A.x) + row * A.x_stride;
+    const uint16_t* g = static_cast<const uint16_t*>(A.gate) + row * A.gate_stride;
     u4_t xv[VPT], gv[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int v = i * TPR + tid;
+        const int k = 8 * (i * TPR + tid), n = K - k;
         xv[i] = gv[i] = u4_t{0, 0, 0, 0};
-        if (v < nv) {
-            xv[i] = x[v];
-            if (GATED) gv[i] = g[v];
+        if (n > 0) {
+            xv[i] = load8(x + k, n);
+            if (GATED) gv[i] = load8(g + k, n);
         }
     }
     // A value in 64 bits, from memory again where it is needed (seldom).
     const auto value64 = [&](int k) {
-        double y = (double)to_float(reinterpret_cast<const uint16_t*>(x)[k], BF16);
-        if (GATED) y *= silu64((double)to_float(reinterpret_cast<const uint16_t*>(g)[k], BF16));
+        double y = (double)to_float(x[k], BF16);
+        if (GATED) y *= silu64((double)to_float(g[k], BF16));
         return y;
     };
     float t[VPT][8], least = 0.0f;
@@ -399,7 +430,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rows_vec_kernel(const R
         double m = 0.0;
         if (slow) {
             bad = false;
-            for (int k = tid; k < 8 * nv; k += TPR) {
+            for (int k = tid; k < K; k += TPR) {
                 const double y = __builtin_fabs(value64(k));
                 m = !(y <= 3.4028234663852886e38) ? __builtin_inf() : y > m ? y : m;
             }
@@ -422,13 +453,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rows_vec_kernel(const R
     }
     const bool zero = most <= 127 * 0x1p-150;                       // most / 127 rounds to 0
     // (gated32 is off by 2^-21 at most, a quotient by 2^-14; in the slow case every code is decided in 64 bits)
-    write_codes<TPR>(t, static_cast<int8_t*>(A.codes) + row * A.codes_stride, nv, bad || zero, slow ? 0.0f : (float)most, most,
+    write_codes<TPR>(t, static_cast<int8_t*>(A.codes) + row * A.codes_stride, K, bad || zero, slow ? 0.0f : (float)most, most,
                      GATED ? 0x1p-13f : 0x1p-14f, value64);
     if (tid == 0) A.scales[row] = bad ? __builtin_nanf("") : zero ? 1.0f : (float)(most / 127.0);
-}
-
-bool by(const void* p, int64_t stride, int64_t bytes, int64_t size) {
-    return reinterpret_cast<uintptr_t>(p) % bytes == 0 && stride * size % bytes == 0;
 }
 
 // Runs f with the row's threads and vectors a thread as constants: two vectors a
@@ -486,10 +513,7 @@ hipError_t launch_norm(const NormCall& all, hipStream_t stream) {
         c.codes = after(all.codes, r * all.codes_stride);
         c.out = after(all.out, 2 * r * all.out_stride);
         c.scales = all.scales ? all.scales + r : nullptr;
-        const bool vec = c.K % 8 == 0 && c.K <= kWidest && by(c.x, c.x_stride, 16, 2) && by(c.residual, c.residual_stride, 16, 2) &&
-                         by(c.weight, 0, 16, 2) && by(c.total, c.total_stride, 16, 2) && by(c.codes, c.codes_stride, 8, 1) &&
-                         by(c.out, c.out_stride, 16, 2);
-        if (!vec) norm_any_kernel<<<dim3((unsigned)c.rows), dim3(kThreads), 0, stream>>>(c);
+        if (c.K > kWidest) norm_any_kernel<<<dim3((unsigned)c.rows), dim3(kThreads), 0, stream>>>(c);
         else if (c.codes && c.bf16) run_norm_vec<MODE_NORM_CODES, true>(c, stream);
         else if (c.codes) run_norm_vec<MODE_NORM_CODES, false>(c, stream);
         else if (c.bf16) run_norm_vec<MODE_NORM_VALUES, true>(c, stream);
@@ -508,9 +532,7 @@ hipError_t launch_rows(const RowsCall& all, hipStream_t stream) {
         c.gate = after(all.gate, 2 * r * all.gate_stride);
         c.codes = after(all.codes, r * all.codes_stride);
         c.scales = all.scales + r;
-        const bool vec = c.K % 8 == 0 && c.K <= kWidest && by(c.x, c.x_stride, 16, 2) && by(c.gate, c.gate_stride, 16, 2) &&
-                         by(c.codes, c.codes_stride, 8, 1);
-        if (!vec) rows_any_kernel<<<dim3((unsigned)c.rows), dim3(kThreads), 0, stream>>>(c);
+        if (c.K > kWidest) rows_any_kernel<<<dim3((unsigned)c.rows), dim3(kThreads), 0, stream>>>(c);
         else if (c.gate && c.bf16) run_rows_vec<MODE_GATED, true>(c, stream);
         else if (c.gate) run_rows_vec<MODE_GATED, false>(c, stream);
         else if (c.bf16) run_rows_vec<MODE_ROWS, true>(c, stream);

@@ -466,9 +466,10 @@ typedef enum {
  *
  * x, gate  16-bit [rows][K], 2-byte aligned, strides in elements in [0, 2^37]
  * codes    stride >= K if rows > 1; scales 4-byte aligned
- * 0 <= rows < 2^24, 1 <= K <= 2^20 (beyond: WQ_ERR_UNSUPPORTED).  With 16-byte
- * aligned x and gate, 8-byte aligned codes, and K and the strides multiples of
- * 8, loads and stores are wide.  Inputs may be infinite or NaN.
+ * 0 <= rows < 2^24, 1 <= K <= 2^20 (beyond: WQ_ERR_UNSUPPORTED).  Up to K =
+ * 32768 loads and stores are 16 bytes wide at any alignment, fastest where rows
+ * begin on 16 bytes; past it they take one value each.  Inputs may be infinite
+ * or NaN.
  */
 wq_status wq_quantize_rows(const void* x, int64_t x_stride, const void* gate, int64_t gate_stride, int64_t rows,
                            int64_t K, int32_t dtype, void* codes, int64_t codes_stride, float* scales, void* stream);
