@@ -152,27 +152,29 @@ enum { MODE_NORM_CODES, MODE_NORM_VALUES, MODE_ROWS, MODE_GATED };
 typedef unsigned int u4_t __attribute__((ext_vector_type(4)));
 typedef unsigned int u2_t __attribute__((ext_vector_type(2)));
 // Global memory takes wide accesses at any address: norms of 8192 rows of 8192 values
-// 88 us, of 8191 133, one value at a time 255.
+// 88 us, of 8191 121, one value at a time 255.
 typedef u4_t u4_any __attribute__((aligned(2)));
 typedef u2_t u2_any __attribute__((aligned(1)));
 
-// Eight values at p, of which the first n exist (n < 8 at a row's end only).
-__device__ __forceinline__ u4_t load8(const uint16_t* p, int n) {
-    if (n >= 8) return *reinterpret_cast<const u4_any*>(p);
+// Eight values at p, of which the first n exist; `tail`: whether rows end inside
+// eight (the same for all threads, so that other rows skip it at once).
+__device__ __forceinline__ u4_t load8(const uint16_t* p, int n, bool tail) {
     u4_t v = {0, 0, 0, 0};
+    if (n >= 8) v = *reinterpret_cast<const u4_any*>(p);
+    if (tail && n > 0 && n < 8) {
 #pragma unroll
-    for (int e = 0; e < 7; ++e)
-        if (e < n) v[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
+        for (int e = 0; e < 7; ++e)
+            if (e < n) v[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
+    }
     return v;
 }
-__device__ __forceinline__ void store8(uint16_t* p, u4_t v, int n) {
-    if (n >= 8) {
-        *reinterpret_cast<u4_any*>(p) = v;
-        return;
-    }
+__device__ __forceinline__ void store8(uint16_t* p, u4_t v, int n, bool tail) {
+    if (n >= 8) *reinterpret_cast<u4_any*>(p) = v;
+    if (tail && n > 0 && n < 8) {
 #pragma unroll
-    for (int e = 0; e < 7; ++e)
-        if (e < n) p[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+        for (int e = 0; e < 7; ++e)
+            if (e < n) p[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+    }
 }
 
 template <bool BF16>
@@ -287,9 +289,8 @@ __device__ __forceinline__ void write_codes(const float (&t)[VPT][8], int8_t* co
         uint32_t near = 0;
         uint2 c = make_uint2(0, 0);
         if (!none) c = codes8(t[i], inv, win, near);
-        if (n >= 8) {
-            *reinterpret_cast<u2_any*>(codes + k) = u2_t{c.x, c.y};
-        } else {
+        if (n >= 8) *reinterpret_cast<u2_any*>(codes + k) = u2_t{c.x, c.y};
+        if ((K & 7) != 0 && n < 8) {
             near &= (1u << n) - 1;
 #pragma unroll
             for (int e = 0; e < 7; ++e)
@@ -313,6 +314,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_vec_kernel(const N
     const int64_t row = (int64_t)blockIdx.x * RPB + (RPB > 1 ? threadIdx.x / TPR : 0);
     if (RPB > 1 && row >= A.rows) return;                           // (a whole wave)
     const int tid = threadIdx.x % TPR, K = (int)A.K;
+    const bool tail = (K & 7) != 0;
     const uint16_t* x = static_cast<const uint16_t*>(A.x) + row * A.x_stride;
     const uint16_t* res = static_cast<const uint16_t*>(A.residual) + row * A.residual_stride;
     const uint16_t* wt = static_cast<const uint16_t*>(A.weight);
@@ -322,12 +324,10 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_vec_kernel(const N
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int k = 8 * (i * TPR + tid), n = K - k;
-        h[i] = b[i] = w[i] = u4_t{0, 0, 0, 0};
-        if (n > 0) {
-            h[i] = load8(x + k, n);
-            if (add) b[i] = load8(res + k, n);
-            w[i] = load8(wt + k, n);
-        }
+        b[i] = u4_t{0, 0, 0, 0};
+        h[i] = load8(x + k, n, tail);
+        if (add) b[i] = load8(res + k, n, tail);
+        w[i] = load8(wt + k, n, tail);
     }
     float t[VPT][8];
     uint32_t top = 0;
@@ -340,7 +340,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_vec_kernel(const N
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[e] = part<BF16>(h[i], e) + part<BF16>(b[i], e);
             h[i] = pack8<BF16>(f);
-            if (n > 0) store8(total + k, h[i], n);
+            store8(total + k, h[i], n, tail);
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -361,7 +361,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_vec_kernel(const N
             float f[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[e] = t[i][e] * r;
-            if (n > 0) store8(out + k, pack8<BF16>(f), n);
+            store8(out + k, pack8<BF16>(f), n, tail);
         }
         return;
     }
@@ -375,8 +375,11 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_vec_kernel(const N
     if (tid == 0) A.scales[row] = !fine ? __builtin_nanf("") : top ? r * amax / 127.0f : 1.0f;
 }
 
-template <int MODE, bool BF16, int TPR, int VPT>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rows_vec_kernel(const RowsCall A) {
+// (WAVES: gated rows of 512 threads are held to registers for another workgroup a
+// compute unit: 8192 x 11008 111 -> 95 us, 4096 x 14336 69 -> 63, 8192 x 8192 74 -> 72;
+// the other widths lose by it, 8192 x 4096 36 -> 38.)
+template <int MODE, bool BF16, int TPR, int VPT, int WAVES = (MODE != MODE_GATED || TPR != 512 ? 1 : VPT == 2 ? 8 : 6)>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR, WAVES) void rows_vec_kernel(const RowsCall A) {
     constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
     constexpr bool GATED = MODE == MODE_GATED;
     __shared__ uint32_t tops[TPR / kWave];
@@ -384,17 +387,15 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rows_vec_kernel(const R
     const int64_t row = (int64_t)blockIdx.x * RPB + (RPB > 1 ? threadIdx.x / TPR : 0);
     if (RPB > 1 && row >= A.rows) return;                           // (a whole wave)
     const int tid = threadIdx.x % TPR, K = (int)A.K;
+    const bool tail = (K & 7) != 0;
     const uint16_t* x = static_cast<const uint16_t*>(A.x) + row * A.x_stride;
     const uint16_t* g = static_cast<const uint16_t*>(A.gate) + row * A.gate_stride;
     u4_t xv[VPT], gv[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int k = 8 * (i * TPR + tid), n = K - k;
-        xv[i] = gv[i] = u4_t{0, 0, 0, 0};
-        if (n > 0) {
-            xv[i] = load8(x + k, n);
-            if (GATED) gv[i] = load8(g + k, n);
-        }
+        xv[i] = load8(x + k, n, tail);
+        gv[i] = GATED ? load8(g + k, n, tail) : u4_t{0, 0, 0, 0};
     }
     // A value in 64 bits, from memory again where it is needed (seldom).
     const auto value64 = [&](int k) {
@@ -461,7 +462,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rows_vec_kernel(const R
 // Runs f with the row's threads and vectors a thread as constants: two vectors a
 // thread, so that several workgroups a compute unit wait for memory by turns.
 // 8192 rows of 8192 with a residual: 512 threads of two 86 us (5.4 TB/s), 256 of four
-// 94, 1024 of one 95; of 11008, gated: 512 of three 97 us (4.6 TB/s), 1024 of two 129,
+// 94, 1024 of one 95; of 11008, gated: 512 of three 95 us (4.7 TB/s), 1024 of two 129,
 // 256 of six 315 (they spill); of 4096: 256 of two 46 us, 512 of one 48, a wave of
 // eight 121; 28672 rows of 8192 without norm 118 us, 6.0 TB/s.  What bounds the norm
 // and the plain rows is HBM, the gated ones the vector units as well (some 30
