@@ -462,7 +462,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, WAVES) void rows_vec_kernel(
 // Runs f with the row's threads and vectors a thread as constants: two vectors a
 // thread, so that several workgroups a compute unit wait for memory by turns.
 // 8192 rows of 8192 with a residual: 512 threads of two 86 us (5.4 TB/s), 256 of four
-// 94, 1024 of one 95; of 11008, gated: 512 of three 95 us (4.7 TB/s), 1024 of two 129,
+// 94, 1024 of one 95; of 4864: 256 of three 61 us, 512 of two 69; of 11008, gated: 512 of three 95 us (4.7 TB/s), 1024 of two 129,
 // 256 of six 315 (they spill); of 4096: 256 of two 46 us, 512 of one 48, a wave of
 // eight 121; 28672 rows of 8192 without norm 118 us, 6.0 TB/s.  What bounds the norm
 // and the plain rows is HBM, the gated ones the vector units as well (some 30
@@ -474,9 +474,11 @@ void with_width(int64_t K, F f) {
     else if (K <= 1024) f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
     else if (K <= 2048) f(integral_constant<int, 256>{}, integral_constant<int, 1>{});
     else if (K <= 4096) f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+    else if (K <= 6144) f(integral_constant<int, 256>{}, integral_constant<int, 3>{});
     else if (K <= 8192) f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
     else if (K <= 12288) f(integral_constant<int, 512>{}, integral_constant<int, 3>{});
     else if (K <= 16384) f(integral_constant<int, 512>{}, integral_constant<int, 4>{});
+    else if (K <= 24576) f(integral_constant<int, 1024>{}, integral_constant<int, 3>{});
     else f(integral_constant<int, 1024>{}, integral_constant<int, 4>{});
 }
 
