@@ -462,10 +462,11 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, WAVES) void rows_vec_kernel(
 // Runs f with the row's threads and vectors a thread as constants: two vectors a
 // thread, so that several workgroups a compute unit wait for memory by turns.
 // 8192 rows of 8192 with a residual: 512 threads of two 86 us (5.4 TB/s), 256 of four
-// 94, 1024 of one 95; of 4864: 256 of three 61 us, 512 of two 69; of 11008, gated: 512 of three 95 us (4.7 TB/s), 1024 of two 129,
-// 256 of six 315 (they spill); of 4096: 256 of two 46 us, 512 of one 48, a wave of
-// eight 121; 28672 rows of 8192 without norm 118 us, 6.0 TB/s.  What bounds the norm
-// and the plain rows is HBM, the gated ones the vector units as well (some 30
+// 94, 1024 of one 95; of 4864: 256 of three 61 us, 512 of two 69; of 11008, gated: 512
+// of three 90 us (5.0 TB/s), 1024 of two 129, 256 of six 315 (they spill); of 4096: 256
+// of two 46 us, 512 of one 48, a wave of eight 121; 2048 rows of 20480 without norm:
+// 1024 of three 26 us, of four 33; 28672 rows of 8192 117 us, 6.0 TB/s.  What bounds the
+// norm and the plain rows is HBM, the gated ones the vector units as well (some 30
 // instructions a value).
 template <class F>
 void with_width(int64_t K, F f) {

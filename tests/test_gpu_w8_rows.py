@@ -24,7 +24,8 @@ pytestmark = pytest.mark.gpu
 # (512 values a step) or one workgroup holds, models' widths.
 SIZES = [(1, 1), (3, 2), (2, 7), (5, 8), (4, 9), (3, 63), (9, 64), (7, 100), (1, 512), (6, 520), (33, 896), (5, 1000),
          (1, 4096), (17, 4096), (3, 4100), (2, 4104), (1, 4864), (3, 5000), (1, 8192), (9, 8192), (2, 8200), (1, 11008),
-         (3, 11008), (2, 16384), (1, 20001), (2, 28672), (1, 32768), (2, 32776), (1, 70000), (1, 131077)]
+         (3, 11008), (2, 16384), (1, 20001), (2, 28672), (1, 32768), (2, 32776), (1, 70000), (1, 131077),
+         (2, 4097), (2, 6144), (2, 6145), (2, 12288), (2, 12289), (2, 16385), (2, 24576), (2, 24577)]
 
 
 def randn(seed, *shape):
