@@ -532,12 +532,14 @@ def _apart(outs, ins):
                     raise ValueError(f"{name} overlaps {other}")
 
 
-def _codes_out(out, x, rows, K, device, inputs):
+def _codes_out(out, x, xs, rows, K, device, inputs):
     """(codes, scales, stride) of a call: new, or the caller's (inputs: as _apart's)."""
     import torch
     if out is None:
-        # (like x: rows that are apart give contiguous ones)
-        return torch.empty_like(x, dtype=torch.int8), x.new_empty(rows, dtype=torch.float32), K
+        # (empty_like is the quickest call; it keeps the order of x's strides, which rows
+        # less than K apart, that repeat or overlap, may have the other way round)
+        codes = torch.empty_like(x, dtype=torch.int8) if xs >= K else x.new_empty((rows, K), dtype=torch.int8)
+        return codes, x.new_empty(rows, dtype=torch.float32), K
     codes, scales = out
     stride = _rows2(codes, torch.int8, rows, K, "codes", device)
     _vector(scales, torch.float32, rows, "scales", device)
@@ -559,7 +561,7 @@ def quantize_rows(x, gate=None, out=None):
     dev = x.device
     xs = _rows2(x, dt, rows, K, "x", dev)
     gs = _rows2(gate, dt, rows, K, "gate", dev) if gate is not None else 0
-    codes, scales, cs = _codes_out(out, x, rows, K, dev, ((x, "x"), (gate, "gate")))
+    codes, scales, cs = _codes_out(out, x, xs, rows, K, dev, ((x, "x"), (gate, "gate")))
     _launch("wq_quantize_rows", dev, load().wq_quantize_rows, x.data_ptr(), xs,
             gate.data_ptr() if gate is not None else None, gs, rows, K, code, codes.data_ptr(), cs, scales.data_ptr())
     return codes, scales
@@ -582,7 +584,7 @@ def _norm_inputs(x, weight, residual, total):
         return code, rows, K, xs, None, 0, None, None, 0
     rs = _rows2(residual, dt, rows, K, "residual", dev)
     if total is None:
-        total = torch.empty_like(x)
+        total = torch.empty_like(x) if xs >= K else x.new_empty((rows, K))         # (as _codes_out)
         ts = K
     else:
         ts = _rows2(total, dt, rows, K, "total", dev)
@@ -601,8 +603,8 @@ def rmsnorm_quantize(x, weight, residual=None, eps: float = 1e-6, total=None, ou
     itself; None without a residual.  out: a (codes, scales) pair."""
     code, rows, K, xs, rp, rs, total, tp, ts = _norm_inputs(x, weight, residual, total)
     dev = x.device
-    codes, scales, cs = _codes_out(out, x, rows, K, dev, ((x, "x"), (weight, "weight"), (residual, "residual"),
-                                                       (total, "total")))
+    codes, scales, cs = _codes_out(out, x, xs, rows, K, dev, ((x, "x"), (weight, "weight"), (residual, "residual"),
+                                                           (total, "total")))
     _launch("wq_rmsnorm_quantize", dev, load().wq_rmsnorm_quantize, x.data_ptr(), xs, rp, rs, weight.data_ptr(), rows, K,
             code, eps, tp, ts, codes.data_ptr(), cs, scales.data_ptr())
     return codes, scales, total
@@ -615,7 +617,7 @@ def rmsnorm(x, weight, residual=None, eps: float = 1e-6, total=None, out=None):
     code, rows, K, xs, rp, rs, total, tp, ts = _norm_inputs(x, weight, residual, total)
     dev = x.device
     if out is None:
-        out = torch.empty_like(x)
+        out = torch.empty_like(x) if xs >= K else x.new_empty((rows, K))
         os_ = K
     else:
         os_ = _rows2(out, x.dtype, rows, K, "out", dev)
