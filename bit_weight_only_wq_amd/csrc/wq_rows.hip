@@ -71,6 +71,19 @@ __device__ __forceinline__ float norm_factor(const NormCall& A, double sum) {
     return mean > 0x1p-100 && mean < 0x1p100 ? 1.0f / __builtin_sqrtf((float)mean) : (float)(1.0 / sqrt(mean));
 }
 
+__device__ __forceinline__ double norm_factor64(const NormCall& A, double sum) {
+    return 1.0 / sqrt(sum * A.per_value + (double)A.eps);
+}
+
+// The norm's value t r, t = h w.  Two bf16 values' product may be past fp32's largest,
+// or lose bits below its smallest normal number, while t r is a bf16 number: then all
+// of it is formed in 64 bits.  A product that is 0 is one of a 0, or less than 2^-149:
+// then t r is 0 in bf16 too unless r is 2^16 at least.
+__device__ __forceinline__ bool past_fp32(float t) { return __builtin_amdgcn_classf(t, 0x294); }   // subnormal or infinite
+__device__ __forceinline__ float norm_value64(uint16_t h, uint16_t w, double r) {
+    return (float)((double)to_float(h, true) * (double)to_float(w, true) * r);
+}
+
 __device__ __forceinline__ double silu64(double g) { return g / (1.0 + exp(-g)); }
 
 // Rows past what registers hold: one workgroup a row, one value at a time.
@@ -97,11 +110,14 @@ __global__ __launch_bounds__(kThreads) void norm_any_kernel(const NormCall A) {
     const bool fine = top < kInfBits && sum < __builtin_inf();
     for (int64_t k = threadIdx.x; k < A.K; k += kThreads) {
         const float t = to_float(h[k], A.bf16) * to_float(w[k], A.bf16);
-        if (A.out)
-            static_cast<uint16_t*>(A.out)[row * A.out_stride + k] = from_float(t * r, A.bf16);
-        else
+        if (A.out) {
+            float y = t * r;
+            if (A.bf16 && (past_fp32(t) || t == 0.0f)) y = norm_value64(h[k], w[k], norm_factor64(A, sum));
+            static_cast<uint16_t*>(A.out)[row * A.out_stride + k] = from_float(y, A.bf16);
+        } else {
             static_cast<int8_t*>(A.codes)[row * A.codes_stride + k] =
                 fine && top ? (int8_t)exact_code((double)t, (double)amax) : (int8_t)0;
+        }
     }
     if (A.codes && threadIdx.x == 0)
         A.scales[row] = !fine ? __builtin_nanf("") : top ? r * amax / 127.0f : 1.0f;
@@ -306,8 +322,10 @@ __device__ __forceinline__ void write_codes(const float (&t)[VPT][8], int8_t* co
     }
 }
 
-template <int MODE, bool BF16, int TPR, int VPT>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_vec_kernel(const NormCall A) {
+// (WAVES: 1024 threads of three vectors, bf16 values, at 64 registers, so that a compute
+// unit holds two workgroups.)
+template <int MODE, bool BF16, int TPR, int VPT, int WAVES = (MODE == MODE_NORM_VALUES && BF16 && TPR == 1024 && VPT == 3 ? 8 : 1)>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR, WAVES) void norm_vec_kernel(const NormCall A) {
     constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
     __shared__ uint32_t tops[TPR / kWave];
     __shared__ double sums[TPR / kWave];
@@ -331,6 +349,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_vec_kernel(const N
     }
     float t[VPT][8];
     uint32_t top = 0;
+    bool past = false;
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -348,11 +367,13 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_vec_kernel(const N
             t[i][e] = f * part<BF16>(w[i], e);
             const uint32_t u = __builtin_bit_cast(uint32_t, t[i][e]) & 0x7FFFFFFFu;
             top = u > top ? u : top;
+            if (MODE == MODE_NORM_VALUES && BF16) past |= past_fp32(t[i][e]);
             sum = __builtin_fma((double)f, (double)f, sum);
         }
     }
     row_join<TPR>(top, sum, tops, sums);
     const float r = norm_factor(A, sum);
+    const uint16_t* from = add ? total : x;
     if constexpr (MODE == MODE_NORM_VALUES) {
         uint16_t* out = static_cast<uint16_t*>(A.out) + row * A.out_stride;
 #pragma unroll
@@ -363,11 +384,23 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_vec_kernel(const N
             for (int e = 0; e < 8; ++e) f[e] = t[i][e] * r;
             store8(out + k, pack8<BF16>(f), n, tail);
         }
+        // What fp32's product does not hold, once all is written (the thread's values one
+        // after another from memory: seldom, and few registers).
+        if (BF16 && (past || r >= 0x1p16f) && sum > 0.0) {
+            const double r64 = norm_factor64(A, sum);
+#pragma clang loop unroll(disable)
+            for (int v = 0; v < 8 * VPT; ++v) {
+                const int k = 8 * ((v >> 3) * TPR + tid) + (v & 7);
+                if (k >= K) break;
+                const uint16_t hk = from[k], wk = wt[k];
+                const float p = to_float(hk, BF16) * to_float(wk, BF16);
+                if (past_fp32(p) || p == 0.0f) out[k] = from_float(norm_value64(hk, wk, r64), BF16);
+            }
+        }
         return;
     }
     const bool fine = top < kInfBits && sum < __builtin_inf();
     const float amax = __builtin_bit_cast(float, top);
-    const uint16_t* from = add ? total : x;
     write_codes<TPR>(t, static_cast<int8_t*>(A.codes) + row * A.codes_stride, K, !fine || !top, amax, (double)amax, 0x1p-14f,
                      [&](int k) {
                          return (double)(to_float(from[k], BF16) * to_float(wt[k], BF16));

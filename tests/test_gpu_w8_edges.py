@@ -48,3 +48,43 @@ def test_rows_that_overlap(dt, R, K, step):
         same(fn(x, w, residual=other), fn(plain, w, residual=other))
         same(fn(other, w, residual=x), fn(other, w, residual=plain))
         same(fn(x, w, residual=x), fn(plain, w, residual=plain))
+
+
+def odd_norm_rows(K, seed):
+    """bf16 rows h and weights w whose products leave what fp32 holds exactly, on
+    either side: past its largest, below its smallest normal, below its smallest, of
+    mixed sizes, rows of zeros and ordinary ones between them."""
+    h = randn(seed, 8, K)
+    h[0] *= 2.0 ** 125                                       # h w past fp32 where w > 2
+    h[1] *= 3e-24
+    h[2] *= 2.0 ** -100
+    h[3] *= torch.exp2(torch.linspace(-120, 0, K))           # a few large, most tiny
+    h[4] = 0.0
+    h[5] = 0.0
+    h[5, K // 2] = 2.0 ** 126
+    h[7, ::2] = 0.0
+    return h.bfloat16()
+
+
+WEIGHTS = {"large": 8.0, "tiny": 1e-18, "least": 2.0 ** -60, "ordinary": 1.0}
+
+
+@pytest.mark.parametrize("K", [1, 7, 64, 1000, 2048, 5000, 8192, 12288, 16384, 20000, 32768, 40000])
+@pytest.mark.parametrize("size", list(WEIGHTS))
+@pytest.mark.parametrize("residual", [False, True])
+def test_values_past_fp32_products(K, size, residual):
+    """The norm's values where h w is no fp32 number but h w / rms is a bf16 one."""
+    dev = device()
+    note(f"norm values, products past fp32, K={K} {size} residual={residual}")
+    h = odd_norm_rows(K, K)
+    w = (WEIGHTS[size] * (1 + 0.3 * randn(K + 1, K))).bfloat16()
+    res = None
+    if residual:
+        h = h / 2                                            # (the sum is what h was)
+        res = h.clone()
+    for eps in (1e-6, 2.0 ** -126):
+        y, _, _, total = w8_util.norm(h, w, res, eps)
+        got, t = wq.rmsnorm(h.to(dev), w.to(dev), residual=res.to(dev) if residual else None, eps=eps)
+        assert np.isfinite(y).all() and np.abs(y).max() < 3e38
+        check_values(got, y, torch.bfloat16, (K, size, eps))
+        assert not residual or torch.equal(bits(t), bits(total))
