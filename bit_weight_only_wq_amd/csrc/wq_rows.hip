@@ -6,8 +6,9 @@
 //     code = round-half-even(127 t / max|t|),   value = code * scale
 // The norm's factor r = 1 / sqrt(mean h^2 + eps) cancels in 127 t / max|t|, so
 // codes do not depend on how the squares were summed; it enters the scale only.
-// h and w have at most 11 significant bits each, so t is exact in fp32.  A code
-// is 127 / max times t in fp32, off by less than 2^-15 (two roundings of a
+// h and w have at most 11 significant bits each, so t is exact in fp32 (two bf16
+// values' below 2^-133 is not: rows whose max is below 2^-100 take their products in
+// fp64, and in other rows such a t has code 0).  A code is 127 / max times t in fp32, off by less than 2^-15 (two roundings of a
 // number up to 127), and wherever that lies near a border between two codes the
 // quotient is formed in fp64.  Without a gate one that is not on the border lies
 // 2^-24 from it at least.  Gated values are off by some 2^-52 in fp64; they have
@@ -57,6 +58,24 @@ __device__ __forceinline__ void block_join(uint32_t& top, double& sum) {
     }
 }
 
+// Largest of a row's TPR threads' values, none below 0, in each of them.
+template <int TPR>
+__device__ __forceinline__ double row_most(double v, double* mosts) {
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+        const double t = __shfl_xor(v, o, kWave);
+        v = t > v ? t : v;
+    }
+    if constexpr (TPR > kWave) {
+        if ((threadIdx.x & 63) == 0) mosts[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = 0.0;
+#pragma unroll
+        for (int w = 0; w < TPR / kWave; ++w) v = mosts[w] > v ? mosts[w] : v;
+    }
+    return v;
+}
+
 // round-half-even(127 t / top), ties as above.
 __device__ __forceinline__ int exact_code(double t, double top) {
     const double q = 127.0 * t / top;
@@ -84,6 +103,14 @@ __device__ __forceinline__ float norm_value64(uint16_t h, uint16_t w, double r) 
     return (float)((double)to_float(h, true) * (double)to_float(w, true) * r);
 }
 
+// A row whose largest |t| is below 2^-100, not all of its h being 0: what fp32 says of
+// its products may be off.
+__device__ __forceinline__ bool small_row(bool bf16, uint32_t top, double sum) { return bf16 && top < 0x0D800000u && sum > 0.0; }
+// The scale of a row's codes, most its largest |t|.
+__device__ __forceinline__ float norm_scale(const NormCall& A, double sum, float r, double most, bool small) {
+    return most == 0.0 ? 1.0f : small ? (float)(norm_factor64(A, sum) * most / 127.0) : r * (float)most / 127.0f;
+}
+
 __device__ __forceinline__ double silu64(double g) { return g / (1.0 + exp(-g)); }
 
 // Rows past what registers hold: one workgroup a row, one value at a time.
@@ -106,8 +133,18 @@ __global__ __launch_bounds__(kThreads) void norm_any_kernel(const NormCall A) {
         sum += (double)v * (double)v;
     }
     block_join(top, sum);
-    const float r = norm_factor(A, sum), amax = __builtin_bit_cast(float, top);
-    const bool fine = top < kInfBits && sum < __builtin_inf();
+    const float r = norm_factor(A, sum);
+    const bool fine = top < kInfBits && sum < __builtin_inf(), small = small_row(A.bf16, top, sum);
+    double most = (double)__builtin_bit_cast(float, top);
+    if (small && A.codes) {
+        double m = 0.0;
+        for (int64_t k = threadIdx.x; k < A.K; k += kThreads) {
+            const double t = __builtin_fabs((double)to_float(h[k], true) * (double)to_float(w[k], true));
+            m = t > m ? t : m;
+        }
+        __shared__ double mosts[kThreads / kWave];
+        most = row_most<kThreads>(m, mosts);
+    }
     for (int64_t k = threadIdx.x; k < A.K; k += kThreads) {
         const float t = to_float(h[k], A.bf16) * to_float(w[k], A.bf16);
         if (A.out) {
@@ -116,11 +153,10 @@ __global__ __launch_bounds__(kThreads) void norm_any_kernel(const NormCall A) {
             static_cast<uint16_t*>(A.out)[row * A.out_stride + k] = from_float(y, A.bf16);
         } else {
             static_cast<int8_t*>(A.codes)[row * A.codes_stride + k] =
-                fine && top ? (int8_t)exact_code((double)t, (double)amax) : (int8_t)0;
+                fine && most > 0.0 ? (int8_t)exact_code((double)to_float(h[k], A.bf16) * (double)to_float(w[k], A.bf16), most) : (int8_t)0;
         }
     }
-    if (A.codes && threadIdx.x == 0)
-        A.scales[row] = !fine ? __builtin_nanf("") : top ? r * amax / 127.0f : 1.0f;
+    if (A.codes && threadIdx.x == 0) A.scales[row] = fine ? norm_scale(A, sum, r, most, small) : __builtin_nanf("");
 }
 
 __global__ __launch_bounds__(kThreads) void rows_any_kernel(const RowsCall A) {
@@ -234,23 +270,6 @@ __device__ __forceinline__ void row_join(uint32_t& top, double& sum, uint32_t* t
     }
 }
 
-template <int TPR>
-__device__ __forceinline__ double row_most(double v, double* mosts) {
-#pragma unroll
-    for (int o = 1; o < kWave; o <<= 1) {
-        const double t = __shfl_xor(v, o, kWave);
-        v = t > v ? t : v;
-    }
-    if constexpr (TPR > kWave) {
-        if ((threadIdx.x & 63) == 0) mosts[threadIdx.x >> 6] = v;
-        __syncthreads();
-        v = 0.0;
-#pragma unroll
-        for (int w = 0; w < TPR / kWave; ++w) v = mosts[w] > v ? mosts[w] : v;
-    }
-    return v;
-}
-
 // x silu(g), off by at most 2^-21 of it for g >= -80 (two instructions of one step of
 // 2^-23, four roundings of 2^-24): exp(-g) as 2^hi (1 + lo ln 2), hi + lo = -g / ln 2
 // in two parts.  Past 100 it is below fp32's half step next to 1.
@@ -328,7 +347,7 @@ template <int MODE, bool BF16, int TPR, int VPT, int WAVES = (MODE == MODE_NORM_
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, WAVES) void norm_vec_kernel(const NormCall A) {
     constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
     __shared__ uint32_t tops[TPR / kWave];
-    __shared__ double sums[TPR / kWave];
+    __shared__ double sums[TPR / kWave], mosts[TPR / kWave];
     const int64_t row = (int64_t)blockIdx.x * RPB + (RPB > 1 ? threadIdx.x / TPR : 0);
     if (RPB > 1 && row >= A.rows) return;                           // (a whole wave)
     const int tid = threadIdx.x % TPR, K = (int)A.K;
@@ -399,13 +418,23 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, WAVES) void norm_vec_kernel(
         }
         return;
     }
-    const bool fine = top < kInfBits && sum < __builtin_inf();
-    const float amax = __builtin_bit_cast(float, top);
-    write_codes<TPR>(t, static_cast<int8_t*>(A.codes) + row * A.codes_stride, K, !fine || !top, amax, (double)amax, 0x1p-14f,
-                     [&](int k) {
-                         return (double)(to_float(from[k], BF16) * to_float(wt[k], BF16));
-                     });
-    if (tid == 0) A.scales[row] = !fine ? __builtin_nanf("") : top ? r * amax / 127.0f : 1.0f;
+    const bool fine = top < kInfBits && sum < __builtin_inf(), small = small_row(BF16, top, sum);
+    const auto value64 = [&](int k) { return (double)to_float(from[k], BF16) * (double)to_float(wt[k], BF16); };
+    double most = (double)__builtin_bit_cast(float, top);
+    if (small) {
+        double m = 0.0;
+#pragma clang loop unroll(disable)
+        for (int v = 0; v < 8 * VPT; ++v) {
+            const int k = 8 * ((v >> 3) * TPR + tid) + (v & 7);
+            if (k >= K) break;
+            const double a = __builtin_fabs(value64(k));
+            m = a > m ? a : m;
+        }
+        most = row_most<TPR>(m, mosts);
+    }
+    write_codes<TPR>(t, static_cast<int8_t*>(A.codes) + row * A.codes_stride, K, !fine || most == 0.0,
+                     __builtin_bit_cast(float, top), most, 0x1p-14f, value64);
+    if (tid == 0) A.scales[row] = fine ? norm_scale(A, sum, r, most, small) : __builtin_nanf("");
 }
 
 // (WAVES: gated rows of 512 threads are held to registers for another workgroup a

@@ -88,3 +88,41 @@ def test_values_past_fp32_products(K, size, residual):
         assert np.isfinite(y).all() and np.abs(y).max() < 3e38
         check_values(got, y, torch.bfloat16, (K, size, eps))
         assert not residual or torch.equal(bits(t), bits(total))
+
+
+@pytest.mark.parametrize("K", [1, 7, 64, 1000, 2048, 5000, 8192, 12288, 16384, 20000, 32768, 40000])
+@pytest.mark.parametrize("size", ["tiny", "least", "ordinary"])
+@pytest.mark.parametrize("residual", [False, True])
+def test_codes_of_products_below_fp32(K, size, residual):
+    """The norm's codes where a row's largest h w is subnormal in fp32, or nothing."""
+    dev = device()
+    note(f"norm codes, products below fp32, K={K} {size} residual={residual}")
+    h = odd_norm_rows(K, K)
+    w = (WEIGHTS[size] * (1 + 0.3 * randn(K + 1, K))).bfloat16()
+    res = None
+    if residual:
+        h = h / 2
+        res = h.clone()
+    for eps in (1e-6, 2.0 ** -126):
+        _, codes, scales, total = w8_util.norm(h, w, res, eps)
+        c, s, t = wq.rmsnorm_quantize(h.to(dev), w.to(dev), residual=res.to(dev) if residual else None, eps=eps)
+        bad = np.argwhere(c.cpu().numpy() != codes)
+        assert not len(bad), (len(bad), bad[0], c.cpu().numpy()[tuple(bad[0])], codes[tuple(bad[0])])
+        # A scale below fp32's smallest normal number: half a step of its own, and the same again for a product before it.
+        got = s.cpu().numpy().astype(np.float64)
+        assert np.all(np.abs(got - scales) <= np.maximum(2.0 ** -21 * scales, 2.0 ** -149)), (got, scales)
+        assert not residual or torch.equal(bits(t), bits(total))
+
+
+def test_codes_next_to_a_border_below_fp32():
+    """127 t / max is 89.228 where the products themselves, rounded to fp32, give 89.243."""
+    dev = device()
+    h = torch.tensor([[3.0e-24, 2.1e-24] + [0.0] * 6]).bfloat16()
+    w = torch.full((8,), 1e-18).bfloat16()
+    rng = np.random.default_rng(5)
+    many = torch.from_numpy(rng.uniform(-3e-24, 3e-24, (64, 2048)).astype(np.float32)).bfloat16()
+    note("codes next to a border below fp32")
+    for x, wt in ((h, w), (many, w[:1].repeat(2048))):
+        _, codes, scales, _ = w8_util.norm(x, wt, None, 2.0 ** -126)
+        c, s, _ = wq.rmsnorm_quantize(x.to(dev), wt.to(dev), eps=2.0 ** -126)
+        check_codes(c, s, codes, scales, 2.0 ** -21, "codes")
