@@ -106,9 +106,12 @@ __device__ __forceinline__ float norm_value64(uint16_t h, uint16_t w, double r) 
 // A row whose largest |t| is below 2^-100, not all of its h being 0: what fp32 says of
 // its products may be off.
 __device__ __forceinline__ bool small_row(bool bf16, uint32_t top, double sum) { return bf16 && top < 0x0D800000u && sum > 0.0; }
-// The scale of a row's codes, most its largest |t|.
-__device__ __forceinline__ float norm_scale(const NormCall& A, double sum, float r, double most, bool small) {
-    return most == 0.0 ? 1.0f : small ? (float)(norm_factor64(A, sum) * most / 127.0) : r * (float)most / 127.0f;
+// The scale of a row's codes, most its largest |t|.  (r most may be past fp32, with a bf16
+// weight past 2^118, where a 127th of it is not.)
+__device__ __forceinline__ float norm_scale(const NormCall& A, bool bf16, double sum, float r, double most, bool small) {
+    if (most == 0.0) return 1.0f;
+    const float y = r * (float)most;
+    return small || (bf16 && y == __builtin_inff()) ? (float)(norm_factor64(A, sum) * most / 127.0) : y / 127.0f;
 }
 
 __device__ __forceinline__ double silu64(double g) { return g / (1.0 + exp(-g)); }
@@ -156,7 +159,7 @@ __global__ __launch_bounds__(kThreads) void norm_any_kernel(const NormCall A) {
                 fine && most > 0.0 ? (int8_t)exact_code((double)to_float(h[k], A.bf16) * (double)to_float(w[k], A.bf16), most) : (int8_t)0;
         }
     }
-    if (A.codes && threadIdx.x == 0) A.scales[row] = fine ? norm_scale(A, sum, r, most, small) : __builtin_nanf("");
+    if (A.codes && threadIdx.x == 0) A.scales[row] = fine ? norm_scale(A, A.bf16, sum, r, most, small) : __builtin_nanf("");
 }
 
 __global__ __launch_bounds__(kThreads) void rows_any_kernel(const RowsCall A) {
@@ -434,7 +437,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, WAVES) void norm_vec_kernel(
     }
     write_codes<TPR>(t, static_cast<int8_t*>(A.codes) + row * A.codes_stride, K, !fine || most == 0.0,
                      __builtin_bit_cast(float, top), most, 0x1p-14f, value64);
-    if (tid == 0) A.scales[row] = fine ? norm_scale(A, sum, r, most, small) : __builtin_nanf("");
+    if (tid == 0) A.scales[row] = fine ? norm_scale(A, BF16, sum, r, most, small) : __builtin_nanf("");
 }
 
 // (WAVES: gated rows of 512 threads are held to registers for another workgroup a

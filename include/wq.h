@@ -481,7 +481,8 @@ wq_status wq_quantize_rows(const void* x, int64_t x_stride, const void* gate, in
  * Without a residual h = x, and total is not written (both are null then).
  * wq_rmsnorm writes y, rounded once; wq_rmsnorm_quantize writes y in 8 bits
  * (above, t = h * weight: the norm's factor is one for the row and cancels in
- * the codes).  Squares are summed in 64 bits.
+ * the codes; a scale below fp32's smallest number is 0).  Squares are summed in
+ * 64 bits.
  *
  * x, residual, total, out  16-bit [rows][K], 2-byte aligned, strides as above;
  *        total may be x or residual itself, at its stride

@@ -126,3 +126,20 @@ def test_codes_next_to_a_border_below_fp32():
         _, codes, scales, _ = w8_util.norm(x, wt, None, 2.0 ** -126)
         c, s, _ = wq.rmsnorm_quantize(x.to(dev), wt.to(dev), eps=2.0 ** -126)
         check_codes(c, s, codes, scales, 2.0 ** -21, "codes")
+
+
+@pytest.mark.parametrize("K", [1024, 2000, 8192, 20000, 40000])
+def test_scale_of_a_lone_large_value(K):
+    """Rows of zeros but for one place: r max is sqrt(K) w there, past fp32, and a
+    127th of it is not."""
+    dev = device()
+    h = torch.zeros((6, K), dtype=torch.bfloat16)
+    w = torch.ones(K, dtype=torch.bfloat16)
+    for i, (value, weight) in enumerate(((4.0, 2.0 ** 125), (2.0 ** -3, 2.0 ** 127), (1.0, -(2.0 ** 127)), (-3.0, 2.0 ** 126),
+                                         (2.0 ** 60, 2.0 ** 67), (1.0, 1.0))):
+        h[i, 7 * i], w[7 * i] = value, weight
+    note(f"scale of a lone large value K={K}")
+    _, codes, scales, _ = w8_util.norm(h, w, None, 1e-6)
+    assert np.isfinite(scales.astype(np.float32)).all() and scales.max() * 127 > 3.5e38
+    c, s, _ = wq.rmsnorm_quantize(h.to(dev), w.to(dev))
+    check_codes(c, s, codes, scales, 2.0 ** -21, K)
