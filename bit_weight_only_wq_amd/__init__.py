@@ -651,7 +651,8 @@ def gemm_w8a8(a, a_scales, w, w_scales, bias=None, dtype=None, out=None, workspa
     16, rows 16-byte aligned.  Y (and bias) is of dtype, float16 or bfloat16: that
     of bias or out if not given, else float16.  Results are the same bits whatever
     the batch and the workspace.  The workspace comes from torch or from
-    `workspace` (gemm_w8a8_workspace); use_workspace=False does without."""
+    `workspace` (gemm_w8a8_workspace; apart from the other tensors);
+    use_workspace=False does without."""
     import torch
     if not isinstance(a, torch.Tensor) or a.dim() != 2 or not isinstance(w, torch.Tensor) or w.dim() != 2 or not a.is_cuda:
         raise ValueError("a must be int8 [B, K] and w int8 [N, K], GPU tensors")

@@ -719,6 +719,12 @@ static wq_status check_w8_shape(int64_t B, int64_t K, int64_t N) {
     return WQ_OK;
 }
 
+// Whether two runs of bytes meet.
+static bool bytes_meet(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+    return b && pa < pb + (uintptr_t)b_bytes && pb < pa + (uintptr_t)a_bytes;
+}
+
 wq_status wq_gemm_w8a8_workspace_size(int64_t B, int64_t K, int64_t N, size_t* bytes) {
     g_last_error[0] = '\0';
     if (!bytes) return fail(WQ_ERR_INVALID_ARG, "wq_gemm_w8a8_workspace_size: null bytes");
@@ -763,6 +769,14 @@ wq_status wq_gemm_w8a8(const void* A, int64_t a_stride, const float* a_scales, c
     // (one row has no stride: the kernels' buffers end by it)
     const wq::W8Call c{A, a_scales, W, w_scales, bias, Y, B, K, N, B > 1 ? a_stride : K, N > 1 ? w_stride : K,
                        B > 1 ? y_stride : N, dtype == WQ_BF16};
+    // The first kernel writes partial sums while others of its workgroups still read.
+    if (workspace && need > 0) {
+        const int64_t n = (int64_t)need;
+        if (bytes_meet(workspace, n, A, (B - 1) * c.a_stride + K) || bytes_meet(workspace, n, W, (N - 1) * c.w_stride + K) ||
+            bytes_meet(workspace, n, Y, 2 * ((B - 1) * c.y_stride + N)) || bytes_meet(workspace, n, a_scales, 4 * B) ||
+            bytes_meet(workspace, n, w_scales, 4 * N) || bytes_meet(workspace, n, bias, 2 * N))
+            return fail(WQ_ERR_INVALID_ARG, "wq_gemm_w8a8: the workspace overlaps an operand or Y");
+    }
     wq::Scratch ws;
     ws.ptr = workspace;
     return check_hip(wq::launch_gemm_w8(c, num_cus(), ws, static_cast<hipStream_t>(stream)), "wq_gemm_w8a8 launch");

@@ -513,7 +513,8 @@ wq_status wq_rmsnorm(const void* x, int64_t x_stride, const void* residual, int6
  * B, N >= 0 (0 is a no-op), B <= 2^20, N <= 2^22; K a multiple of 16 below
  * 2^17 (WQ_ERR_UNSUPPORTED otherwise).
  * Workspace (wq_gemm_w8a8_workspace_size): int32 partial sums where K is split
- * to fill the GPU; without one K is not split.
+ * to fill the GPU, apart from the operands and Y (WQ_ERR_INVALID_ARG); without one
+ * K is not split.
  */
 wq_status wq_gemm_w8a8(const void* A, int64_t a_stride, const float* a_scales, const void* W, int64_t w_stride,
                        const float* w_scales, const void* bias, void* Y, int64_t y_stride, int64_t B, int64_t K,

@@ -143,3 +143,34 @@ def test_scale_of_a_lone_large_value(K):
     assert np.isfinite(scales.astype(np.float32)).all() and scales.max() * 127 > 3.5e38
     c, s, _ = wq.rmsnorm_quantize(h.to(dev), w.to(dev))
     check_codes(c, s, codes, scales, 2.0 ** -21, K)
+
+
+def test_workspace_beside_the_operands():
+    """A workspace right between a and w of one buffer, and right behind Y, is used; over
+    them it is refused."""
+    dev = device()
+    B, K, N = 48, 8192, 1024
+    n = wq.gemm_w8a8_workspace(B, N, K).numel()
+    assert n > 0 and n % 16 == 0
+    y_bytes = 2 * B * N
+    buf = torch.empty(B * K + n + N * K + y_bytes + n, dtype=torch.uint8, device=dev)
+    a = buf[:B * K].view(torch.int8).view(B, K)
+    ws = buf[B * K:B * K + n]
+    w = buf[B * K + n:B * K + n + N * K].view(torch.int8).view(N, K)
+    y = buf[B * K + n + N * K:][:y_bytes].view(torch.float16).view(B, N)
+    ws2 = buf[-n:]
+    rng = np.random.default_rng(1)
+    ha, hw = rng.integers(-128, 128, (B, K)).astype(np.int8), rng.integers(-128, 128, (N, K)).astype(np.int8)
+    sa, sw = torch.full((B,), 2.0 ** -7, device=dev), torch.full((N,), 2.0 ** -9, device=dev)
+    a.copy_(torch.from_numpy(ha))
+    w.copy_(torch.from_numpy(hw))
+    want = w8_util.product(ha, sa.cpu().numpy(), hw, sw.cpu().numpy(), None, torch.float16)
+    for space in (ws, ws2):
+        note("workspace beside the operands")
+        y.zero_()
+        wq.gemm_w8a8(a, sa, w, sw, out=y, workspace=space)
+        assert torch.equal(bits(y), bits(want))
+        assert (a.cpu().numpy() == ha).all() and (w.cpu().numpy() == hw).all()
+    for lo in (0, B * K - 16, B * K + 16, B * K + n + N * K - 16, buf.numel() - n - 16):
+        with pytest.raises(wq.WQError):
+            wq.gemm_w8a8(a, sa, w, sw, out=y, workspace=buf[lo:lo + n])
