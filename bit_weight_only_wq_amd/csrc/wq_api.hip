@@ -5,6 +5,7 @@
 // per-tensor maximum) comes from a caller-owned workspace sized by the
 // wq_*_workspace_size queries, and calls without one take plans that need
 // none.
+#include <float.h>
 #include <stdio.h>
 #include <string.h>
 
@@ -653,7 +654,7 @@ static wq_status run_norm(const char* who, const wq::NormCall& c, int32_t dtype,
     g_last_error[0] = '\0';
     const wq_status st = check_rows_shape(who, c.rows, c.K, dtype);
     if (st != WQ_OK) return st;
-    if (!(c.eps >= 0x1p-126f) || c.eps > 3.4e38f)
+    if (!(c.eps >= FLT_MIN && c.eps <= FLT_MAX))
         return fail(WQ_ERR_INVALID_ARG, "rmsnorm: eps must be finite and at least 2^-126");
     if (!row_strides_ok(c.rows, c.K, c.x_stride, false) || !row_strides_ok(c.rows, c.K, c.residual_stride, false) ||
         !row_strides_ok(c.rows, c.K, c.total_stride, c.total) || !row_strides_ok(c.rows, c.K, c.codes_stride, c.codes) ||

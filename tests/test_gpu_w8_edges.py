@@ -174,3 +174,13 @@ def test_workspace_beside_the_operands():
     for lo in (0, B * K - 16, B * K + 16, B * K + n + N * K - 16, buf.numel() - n - 16):
         with pytest.raises(wq.WQError):
             wq.gemm_w8a8(a, sa, w, sw, out=y, workspace=buf[lo:lo + n])
+
+
+@pytest.mark.parametrize("eps", [2.0 ** -126, 3.4028234663852886e38])
+def test_eps_at_its_ends(eps):
+    dev = device()
+    x, w = randn(1, 5, 1000).bfloat16(), (1 + 0.3 * randn(2, 1000)).bfloat16()
+    y, codes, scales, _ = w8_util.norm(x, w, None, eps)
+    note(f"eps {eps}")
+    check_values(wq.rmsnorm(x.to(dev), w.to(dev), eps=eps)[0], y, torch.bfloat16, "values")
+    check_codes(*wq.rmsnorm_quantize(x.to(dev), w.to(dev), eps=eps)[:2], codes, scales, 2.0 ** -21, "codes")

@@ -7,7 +7,7 @@ import pytest
 
 wq = pytest.importorskip("bit_weight_only_wq_amd")
 from bit_weight_only_wq_amd import _lib  # noqa: E402
-from test_w8_abi import FAKE, at, gemm  # noqa: E402
+from test_w8_abi import FAKE, at, gemm, normq, normv  # noqa: E402
 
 # 48 rows on 1024 x 8192: K is split, so the workspace is written.  Rows of A and W a
 # little apart, Y too.
@@ -26,3 +26,14 @@ def test_workspace_over_an_operand(name):
     for p in (first, last, (first + last) // 32 * 16, first - n.value // 32 * 16, first - (n.value - 1) // 16 * 16):
         assert gemm(**CALL, p=p, n=n.value) == _lib.WQ_ERR_INVALID_ARG, (name, p - FAKE)
         assert b"overlaps" in wq.load().wq_last_error()
+
+
+LARGEST = 3.4028234663852886e38                                # fp32's
+
+
+@pytest.mark.parametrize("eps,want", [(2.0 ** -126, _lib.WQ_OK), (1e-6, _lib.WQ_OK), (3.4e38, _lib.WQ_OK), (3.4025e38, _lib.WQ_OK),
+                                      (LARGEST, _lib.WQ_OK), (float("inf"), _lib.WQ_ERR_INVALID_ARG),
+                                      (2.0 ** -126 - 2.0 ** -149, _lib.WQ_ERR_INVALID_ARG)])
+def test_eps_from_end_to_end(eps, want):
+    """Calls of no rows: eps is looked at, nothing is launched."""
+    assert normq(R=0, eps=eps) == want and normv(R=0, eps=eps) == want
