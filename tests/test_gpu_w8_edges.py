@@ -9,6 +9,7 @@ import pytest
 
 import w8_util
 from gpu_util import device, note
+import test_gpu_w8_rows as rows_tests
 from test_gpu_w8_rows import check_codes, check_values, randn
 from w8_util import TYPES, bits
 
@@ -184,3 +185,58 @@ def test_eps_at_its_ends(eps):
     note(f"eps {eps}")
     check_values(wq.rmsnorm(x.to(dev), w.to(dev), eps=eps)[0], y, torch.bfloat16, "values")
     check_codes(*wq.rmsnorm_quantize(x.to(dev), w.to(dev), eps=eps)[:2], codes, scales, 2.0 ** -21, "codes")
+
+
+# Both ends of every class of widths that a row's threads and vectors are chosen by,
+# where the sizes of test_gpu_w8_rows have a gap.
+WIDTHS = [(3, 511), (3, 513), (3, 1023), (5, 1024), (3, 1025), (4, 1536), (3, 2047), (5, 2048), (3, 2049), (2, 4095), (2, 6143),
+          (2, 8191), (2, 8193), (2, 12287), (2, 16383), (2, 24575), (2, 32767), (2, 32769)]
+
+
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+@pytest.mark.parametrize("R,K", WIDTHS)
+@pytest.mark.parametrize("gate", [False, True])
+def test_rows_at_the_widths_ends(R, K, dt, gate):
+    rows_tests.test_rows_match_definition(R, K, dt, gate)
+
+
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+@pytest.mark.parametrize("R,K", WIDTHS)
+@pytest.mark.parametrize("residual", [False, True])
+def test_norms_at_the_widths_ends(R, K, dt, residual):
+    rows_tests.test_norms_match_definition(R, K, dt, residual)
+
+
+def test_calls_follow_their_stream():
+    """Inputs that a stream of its own writes late: every call on it waits for them, as a
+    launch on another stream would not."""
+    dev, side = device(), torch.cuda.Stream()
+    R, K, N = 6, 4096, 256
+    busy = torch.zeros((4096, 4096), dtype=torch.float16, device=dev)
+    new_x, new_r = randn(1, R, K).half(), randn(2, R, K).half()
+    x, r = torch.zeros((R, K), dtype=torch.float16, device=dev), torch.zeros((R, K), dtype=torch.float16, device=dev)
+    from_x, from_r = new_x.to(dev), new_r.to(dev)
+    w = (1 + 0.3 * randn(3, K)).half()
+    wd = w.to(dev)
+    mat, mat_scales = wq.quantize_rows((0.02 * randn(4, N, K)).half().to(dev))
+    torch.mm(busy, busy)
+    torch.cuda.synchronize()
+    note("calls on a stream of their own")
+    with torch.cuda.stream(side):
+        for _ in range(100):
+            torch.mm(busy, busy)
+        x.copy_(from_x)
+        r.copy_(from_r)
+        codes, scales, total = wq.rmsnorm_quantize(x, wd, residual=r)
+        values, total2 = wq.rmsnorm(x, wd, residual=r)
+        c2, s2 = wq.quantize_rows(total, gate=x)
+        y = wq.gemm_w8a8(codes, scales, mat, mat_scales)
+    side.synchronize()
+    want, want_codes, want_scales, h = w8_util.norm(new_x, w, new_r, 1e-6)
+    check_codes(codes, scales, want_codes, want_scales, 2.0 ** -21, "codes")
+    check_values(values, want, torch.float16, "values")
+    assert torch.equal(bits(total), bits(h)) and torch.equal(bits(total2), bits(h))
+    check_codes(c2, s2, *w8_util.rows(h, new_x), 2.0 ** -22, "gated")
+    product = w8_util.product(codes.cpu().numpy(), scales.cpu().numpy(), mat.cpu().numpy(), mat_scales.cpu().numpy(), None,
+                              torch.float16)
+    assert torch.equal(bits(y), bits(product))
