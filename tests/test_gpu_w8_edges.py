@@ -240,3 +240,24 @@ def test_calls_follow_their_stream():
     product = w8_util.product(codes.cpu().numpy(), scales.cpu().numpy(), mat.cpu().numpy(), mat_scales.cpu().numpy(), None,
                               torch.float16)
     assert torch.equal(bits(y), bits(product))
+
+
+@pytest.mark.parametrize("K", [64, 2048, 11008, 28672, 40000])
+def test_gates_below_the_smallest_normal(K):
+    """bf16 gates that are subnormal, times values so large that the products are ordinary
+    numbers: every code as the exact quotient decides it."""
+    dev = device()
+    rng = np.random.default_rng(K)
+    g = (rng.integers(-127, 128, (6, K)) * 2.0 ** -133).astype(np.float32)
+    g = torch.from_numpy(g).bfloat16()
+    x = randn(K, 6, K) * 2.0 ** 90
+    x[1] = 2.0 ** 75 * randn(K + 1, K)
+    x[2] = 2.0 ** 120
+    x[3] *= 2.0 ** -80
+    g[4] *= 2.0 ** 4
+    g[5, ::2] = 3.0
+    x[5, ::2] = 2.0 ** -44
+    x = x.bfloat16()
+    note(f"subnormal gates K={K}")
+    codes, scales = wq.quantize_rows(x.to(dev), gate=g.to(dev))
+    check_codes(codes, scales, *w8_util.rows(x, g), 2.0 ** -22, K)
