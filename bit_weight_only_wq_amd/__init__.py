@@ -21,7 +21,7 @@ import math
 from operator import attrgetter
 
 from . import roofline  # noqa: F401  (pure arithmetic, no GPU)
-from ._lib import (WQ_PATH_AUTO, WQ_PATH_GEMV, WQ_PATH_MFMA, WQError,  # noqa: F401
+from ._lib import (WQ_BF16, WQ_FP16, WQ_PATH_AUTO, WQ_PATH_GEMV, WQ_PATH_MFMA, WQError,  # noqa: F401
                    LIB_PATH, check, load)
 
 __all__ = ["quantize_pack", "gemm", "gemm_grouped", "gemm_workspace_bytes", "codes_bytes", "num_groups",
@@ -482,9 +482,9 @@ def _dtype(t, name):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
     if t.dtype == torch.float16:
-        return t.dtype, 0
+        return t.dtype, WQ_FP16
     if t.dtype == torch.bfloat16:
-        return t.dtype, 1
+        return t.dtype, WQ_BF16
     raise ValueError(f"{name} must be float16 or bfloat16, got {t.dtype}")
 
 
@@ -681,7 +681,7 @@ def gemm_w8a8(a, a_scales, w, w_scales, bias=None, dtype=None, out=None, workspa
     wp, wn = _given(workspace, dev) if workspace is not None and use_workspace else (None, 0)
     _launch("wq_gemm_w8a8", dev, load().wq_gemm_w8a8, a.data_ptr(), as_, a_scales.data_ptr(), w.data_ptr(), ws_,
             w_scales.data_ptr(), bias.data_ptr() if bias is not None else None, out.data_ptr(), ys, B, K, N,
-            1 if dtype is torch.bfloat16 else 0, wp, wn)
+            WQ_BF16 if dtype is torch.bfloat16 else WQ_FP16, wp, wn)
     return out
 
 

@@ -37,3 +37,12 @@ LARGEST = 3.4028234663852886e38                                # fp32's
 def test_eps_from_end_to_end(eps, want):
     """Calls of no rows: eps is looked at, nothing is launched."""
     assert normq(R=0, eps=eps) == want and normv(R=0, eps=eps) == want
+
+
+def test_type_numbers():
+    """The binding's numbers of the 16-bit types are wq.h's."""
+    import os
+    import re
+    header = open(os.path.join(os.path.dirname(__file__), "..", "include", "wq.h")).read()
+    for name in ("WQ_FP16", "WQ_BF16"):
+        assert int(re.search(name + r" = (\d+)", header).group(1)) == getattr(_lib, name)
