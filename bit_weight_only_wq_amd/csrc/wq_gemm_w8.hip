@@ -570,7 +570,9 @@ struct W8Plan {
 
 // Sizes of a variant, workgroups a compute unit holds, and what it costs in us:
 // first, and for each step with that many (1, 2, 3) workgroups on every compute
-// unit.  Fitted to B = 48 .. 2048 on nine matrices, 512 x 512 to 28672 x 8192.
+// unit.  Fitted to B = 48 .. 2048 on nine matrices, 512 x 512 to 28672 x 8192.  What it
+// takes now for K = 4096: N = 4096, B = 100, 200, 500, 1000: 9.6, 14, 18, 26 us; N = 12288:
+// 18, 24, 40, 57; N = 22016: 31, 43, 61, 121.
 struct W8Cost {
     W8Shape shape;
     int bm, bn, fit;
@@ -584,12 +586,15 @@ constexpr W8Cost kCosts[] = {
 
 int64_t w8_ceil(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Up to 64 rows what counts is that all of the GPU reads W: the widest tile that
-// still gives about one workgroup a compute unit.  One row, N = 4096, K = 4096: 32 rows
-// of W a workgroup 7 us, 64: 8.5, 128: 11.  One row, N = 28672, K = 8192: 128 rows 42 us,
-// 64: 44, 32: 46.  K is split where that leaves compute units idle, into parts of 16
-// steps at least: N = 1024, K = 8192 in four parts 7.7 us, in one 11; N = 4096, K = 4096
-// in two 7.9, in one 6.9.  Past 64 rows the least of the costs above: B = 333, K =
+// Up to 64 rows what counts is that all of the GPU reads W: the narrowest tile that
+// needs no more than one workgroup a compute unit, the widest where all need more.  One
+// row, N = 4096, K = 4096: 32 rows of W a workgroup 7 us, 64: 8.5, 128: 11.  One row, N =
+// 28672, K = 8192: 128 rows 42 us, 64: 44, 32: 46.  Right past a tile's last size half of
+// the compute units are idle: one row, K = 8192: N = 8192 takes 15 us (256 workgroups),
+// 8224 22 (129), 10240 25 (160), 16384 28 (256), 16448 33 (129), 20480 35 (160).  K is split
+// where that leaves compute units idle, into parts of 16 steps at least (but for tiles of
+// 128 rows of W, and those of 64 up to 32 rows): N = 1024, K = 8192 in four parts 7.7 us,
+// in one 11; N = 4096, K = 4096 in two 7.9, in one 6.9.  Past 64 rows the least of the costs above: B = 333, K =
 // 11008, N = 4096 takes 128 x 128 in two parts, 33 us (128 x 64 in one: 35; 64 x 64: 39;
 // 256 x 256: 108).
 W8Plan w8_plan(int64_t B, int64_t K, int64_t N, int cus, bool scratch) {

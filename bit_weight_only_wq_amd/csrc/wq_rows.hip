@@ -116,7 +116,9 @@ __device__ __forceinline__ float norm_scale(const NormCall& A, bool bf16, double
 
 __device__ __forceinline__ double silu64(double g) { return g / (1.0 + exp(-g)); }
 
-// Rows past what registers hold: one workgroup a row, one value at a time.
+// Rows past what registers hold: one workgroup a row, one value at a time, each read
+// twice.  2048 rows of 53248: 440 us with a residual (1.7 TB/s), 280 without norm, 619
+// gated (exp in 64 bits, twice); 64 such rows, on as many compute units, 149, 81 and 154.
 __global__ __launch_bounds__(kThreads) void norm_any_kernel(const NormCall A) {
     const int64_t row = blockIdx.x;
     const uint16_t* x = static_cast<const uint16_t*>(A.x) + row * A.x_stride;
@@ -206,8 +208,8 @@ enum { MODE_NORM_CODES, MODE_NORM_VALUES, MODE_ROWS, MODE_GATED };
 
 typedef unsigned int u4_t __attribute__((ext_vector_type(4)));
 typedef unsigned int u2_t __attribute__((ext_vector_type(2)));
-// Global memory takes wide accesses at any address: norms of 8192 rows of 8192 values
-// 88 us, of 8191 121, one value at a time 255.
+// Global memory takes wide accesses at any address: 8192 rows with a residual, of 8192
+// values 88 us, of 8191 130, one value at a time 255; gated, of 11008 91, of 11007 147.
 typedef u4_t u4_any __attribute__((aligned(2)));
 typedef u2_t u2_any __attribute__((aligned(1)));
 
@@ -484,7 +486,10 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, WAVES) void rows_vec_kernel(
             top = u > top ? u : top;
         }
     const float mine = __builtin_bit_cast(float, top);
-    if (GATED && least < -80.0f) top = 0x80000000u;                 // (exp(-gate) may leave fp32's range: the row goes in 64 bits)
+    // (exp(-gate) may leave fp32's range: the row goes in 64 bits.  So does one whose products
+    // are all small, rows of zeros among them.  8192 x 11008: 91 to 107 us, one such gate in
+    // every row 431, rows of zeros 212.)
+    if (GATED && least < -80.0f) top = 0x80000000u;
     double none = 0.0;
     row_join<TPR>(top, none, tops, sums);
     double most = (double)__builtin_bit_cast(float, top);
@@ -525,7 +530,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR, WAVES) void rows_vec_kernel(
 }
 
 // Runs f with the row's threads and vectors a thread as constants: two vectors a
-// thread, so that several workgroups a compute unit wait for memory by turns.
+// thread, so that several workgroups a compute unit wait for memory by turns.  (Times
+// that are compared were taken together; a long burst's are 5 to 10 % lower than those
+// of its first hundred calls, as the clock rises.)
 // 8192 rows of 8192 with a residual: 512 threads of two 86 us (5.4 TB/s), 256 of four
 // 94, 1024 of one 95; of 4864: 256 of three 61 us, 512 of two 69; of 11008, gated: 512
 // of three 90 us (5.0 TB/s), 1024 of two 129, 256 of six 315 (they spill); of 4096: 256

@@ -465,7 +465,8 @@ typedef enum {
  * widen the scales.)
  *
  * x, gate  16-bit [rows][K], 2-byte aligned, strides in elements in [0, 2^37]
- * codes    stride >= K if rows > 1; scales 4-byte aligned
+ * codes    stride >= K if rows > 1; scales 4-byte aligned; both apart from the
+ *          inputs and each other
  * 0 <= rows < 2^24, 1 <= K <= 2^20 (beyond: WQ_ERR_UNSUPPORTED).  Up to K =
  * 32768 loads and stores are 16 bytes wide at any alignment, fastest where rows
  * begin on 16 bytes; past it they take one value each.  Inputs may be infinite
@@ -485,7 +486,8 @@ wq_status wq_quantize_rows(const void* x, int64_t x_stride, const void* gate, in
  * 64 bits.
  *
  * x, residual, total, out  16-bit [rows][K], 2-byte aligned, strides as above;
- *        total may be x or residual itself, at its stride
+ *        total may be x or residual itself, at its stride; outputs are apart from
+ *        the inputs otherwise, and from each other.  Rows of inputs may repeat or overlap.
  * weight 16-bit [K];  eps in [2^-126, fp32's largest]
  * Sizes, wide loads and non-finite inputs as wq_quantize_rows (wq_rmsnorm: a NaN
  * makes its row NaN, an infinity makes its place NaN and the row's others 0).
@@ -509,7 +511,7 @@ wq_status wq_rmsnorm(const void* x, int64_t x_stride, const void* residual, int6
  *          bytes, multiples of 16 in [K, 2^22]
  * a_scales, w_scales fp32 [B], [N];  bias 16-bit [N] of Y's type, or null
  * Y        16-bit [B][N] (dtype), 2-byte aligned, y_stride elements in
- *          [N, 2^22]
+ *          [N, 2^22], apart from the operands
  * B, N >= 0 (0 is a no-op), B <= 2^20, N <= 2^22; K a multiple of 16 below
  * 2^17 (WQ_ERR_UNSUPPORTED otherwise).
  * Workspace (wq_gemm_w8a8_workspace_size): int32 partial sums where K is split
